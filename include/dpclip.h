@@ -70,6 +70,7 @@ typedef enum {
 } dp_status;
 
 typedef enum { DP_F32 = 0, DP_BF16 = 1 } dp_dtype;
+typedef enum { DP_I32 = 0, DP_I64 = 1 } dp_index; /* integer type of token ids */
 
 /* How n_i is computed.  Both methods give the same value up to rounding:
  *   GHOST    : n_i^2 = sum_{t,s} (x_t . x_s)(dy_t . dy_s), from the two T x T Gram matrices of
@@ -301,6 +302,111 @@ dp_status dp_projected_adam_step(float* W, const float* R, float* m, float* v, c
                                  float beta2, float eps, float grad_scale, int t, void* workspace,
                                  size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ embedding table
+ * The table W[V, d] of an embedding y_n = scale W[id_n], the parameter beside the linears.
+ * ids is [B, T] (token t of sample i at i*T + t), DEVICE int32 or int64 (`it`).  Sample i's
+ * gradient of row v is
+ *   G_i[v] = scale * sum of dY[i, t] over the sample's tokens t with id v,
+ * and the privatised gradient is that of a linear's weight: n_i = ||G_i||, c_i = min(1, C/n_i),
+ * sum_i c_i G_i + sigma*C*z with z over the flat [V, d] output (FlashDP Abstract: per-layer
+ * clipped DP-SGD; the pages treat linears only).  It is the linear step of a one-hot X of V
+ * columns, without forming one: the tokens are sorted by id.
+ *   - A token belongs to no row when its id is negative, equal to padding_idx, or >= V; an id
+ *     >= V is also recorded, and dp_workspace_status then returns DP_ERR_INVALID_ARG.
+ *     padding_idx = -1 (or any value that is no id): no padding row.
+ *   - d is a multiple of 8 (bf16) or 4 (fp32); B*T < 2^31; V*d <= 2^34; scale is finite.
+ *   - Results are the same bits on every run.  A row that no token names gets the noise alone
+ *     (the noise of a private step covers every row). */
+
+/* Y[n] = scale W[ids[n]] for n < N, formed in fp32 and rounded once; ids outside [0, V) give a
+ * row of zeros.  (The padding row is looked up like any other.)
+ *   W : DEVICE [V, d] in w_dt; Y : DEVICE [N, d] in y_dt, overwritten; d a multiple of 8 when
+ *   either is bf16, else of 4. */
+dp_status dp_embedding_lookup(const void* W, dp_dtype w_dt, const void* ids, dp_index it, float scale,
+                              long long N, int V, int d, void* Y, dp_dtype y_dt, void* stream);
+
+/* Workspace bytes of the three calls below (0 when the shape is invalid): about
+ * 4 B*T (6 + d/256) + B*T d/4 + 8 V bytes. */
+size_t dp_embedding_workspace_size(int B, int T, int V, int d, dp_dtype dt);
+
+/* norms[i] = ||G_i||, as dp_per_sample_norms. */
+dp_status dp_embedding_per_sample_norms(const void* ids, dp_index it, const void* dY, dp_dtype dt,
+                                        int B, int T, int V, int d, float scale, long long padding_idx,
+                                        float* norms, void* workspace, size_t ws_bytes, void* stream);
+
+/* G_sum[V, d] += sum_i c_i G_i for given norms (this table's, or flat ones), no noise, as
+ * dp_clip_accumulate.  Rows that no token names are not touched. */
+dp_status dp_embedding_clip_accumulate(const void* ids, dp_index it, const void* dY, dp_dtype dt,
+                                       int B, int T, int V, int d, float scale, long long padding_idx,
+                                       const float* norms, float C, float* G_sum, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/* The privatised step, as dp_linear_step: norms_out[i] = n_i (NULL or DEVICE fp32 [B]) and
+ * G_out = sum_i c_i G_i + sigma*C*z (DEVICE fp32 [V, d], overwritten).  The noise is added in
+ * fp64 and rounded once. */
+dp_status dp_embedding_step(const void* ids, dp_index it, const void* dY, dp_dtype dt, int B, int T,
+                            int V, int d, float scale, long long padding_idx, float C, float sigma,
+                            unsigned long long seed, unsigned long long step, unsigned layer_id,
+                            float* norms_out, float* G_out, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* dp_embedding_step with the step number in device memory (see dp_linear_step_dev_step; no call
+ * before the capture is needed). */
+dp_status dp_embedding_step_dev_step(const void* ids, dp_index it, const void* dY, dp_dtype dt, int B,
+                                     int T, int V, int d, float scale, long long padding_idx, float C,
+                                     float sigma, unsigned long long seed,
+                                     const unsigned long long* step_dev, unsigned layer_id,
+                                     float* norms_out, float* G_out, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* ------------------------------------------------------------------ RMS norm
+ * h = x + residual (rounded to dt), y = h / sqrt(mean(h^2) + eps) * gain, row by row, and its
+ * backward with the privatised gradient of the gain, the remaining parameter of a transformer
+ * block (the pages treat linears only; the reading is that of the linear step):
+ *   g_i[j] = sum_t dY[i,t,j] h[i,t,j] r[i,t],  r = 1 / sqrt(mean(h^2) + eps),
+ *   n_i = ||g_i||, c_i = min(1, C/n_i), sum_i c_i g_i + sigma*C*z with z over the d columns.
+ *   - gain is DEVICE fp32 [d].  The other tensors are in dt.  A row is at most 32 KB (d <= 16384
+ *     in bf16, 8192 in fp32; DP_ERR_UNSUPPORTED above), B <= 65535, eps >= 0 and finite.
+ *   - Outputs must not be inputs of the same call (DP_ERR_INVALID_ARG).
+ *   - Results are the same bits on every run. */
+
+/*   X, residual : [rows, d]; residual NULL: h is X itself, and H is not written.
+ *   H           : [rows, d], needed with residual: the sum, which the backward reads.
+ *   Y           : [rows, d], overwritten. */
+dp_status dp_rmsnorm(const void* X, const void* residual, const float* gain, dp_dtype dt, long long rows,
+                     int d, float eps, void* H, void* Y, void* stream);
+
+/* Workspace bytes of dp_rmsnorm_backward and dp_rmsnorm_step (0 when the shape is invalid). */
+size_t dp_rmsnorm_workspace_size(int B, int T, int d, dp_dtype dt);
+
+/* The backward without privatising, for flat clipping (the norms of a block are combined before
+ * anything is clipped):
+ *   dX[B, T, d]   = the gradient of h, plus residual_grad when given (the gradient that reaches
+ *                   h past the norm); it is the gradient of x and of the residual alike.
+ *   per_sample    : DEVICE fp32 [B, d], the gain gradients g_i; norms : DEVICE fp32 [B]. */
+dp_status dp_rmsnorm_backward(const void* H, const float* gain, const void* dY, const void* residual_grad,
+                              dp_dtype dt, int B, int T, int d, float eps, void* dX, float* per_sample,
+                              float* norms, void* workspace, size_t ws_bytes, void* stream);
+
+/* G_sum[d] += sum_i c_i per_sample[i], c_i = min(1, C / norms[i]), no noise (d a multiple of 4). */
+dp_status dp_rmsnorm_clip_accumulate(const float* per_sample, const float* norms, int B, int d, float C,
+                                     float* G_sum, void* stream);
+
+/* The backward and the privatised gain gradient in one call: dX as above, norms_out (NULL or
+ * DEVICE fp32 [B]) and G_out = sum_i c_i g_i + sigma*C*z (DEVICE fp32 [d], overwritten). */
+dp_status dp_rmsnorm_step(const void* H, const float* gain, const void* dY, const void* residual_grad,
+                          dp_dtype dt, int B, int T, int d, float eps, float C, float sigma,
+                          unsigned long long seed, unsigned long long step, unsigned layer_id, void* dX,
+                          float* norms_out, float* G_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* dp_rmsnorm_step with the step number in device memory. */
+dp_status dp_rmsnorm_step_dev_step(const void* H, const float* gain, const void* dY,
+                                   const void* residual_grad, dp_dtype dt, int B, int T, int d, float eps,
+                                   float C, float sigma, unsigned long long seed,
+                                   const unsigned long long* step_dev, unsigned layer_id, void* dX,
+                                   float* norms_out, float* G_out, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
 /* Failure-detection self-test of the bounded in-kernel waits: a one-warp kernel waits on a
  * barrier that nothing arrives at.  After limit_ns nanoseconds (1 us .. 2 s) it gives up,
  * records the timeout in the workspace's status word and returns.  dp_workspace_status then
@@ -320,7 +426,8 @@ dp_status dp_selftest_fail_launches(long long skip, long long count, int cuda_er
 
 /* Synchronises `stream`, then reads the status word that the kernels of earlier calls wrote
  * into `workspace`.  Returns DP_OK, DP_ERR_TIMEOUT (a bounded in-kernel wait ran out; the
- * results of that call are invalid), DP_ERR_DEVICE_CHECK or DP_ERR_CUDA.  The word is cleared
+ * results of that call are invalid), DP_ERR_INVALID_ARG (a token id of an embedding call was past
+ * the table's end), DP_ERR_DEVICE_CHECK or DP_ERR_CUDA.  The word is cleared
  * at the start of every call that takes a workspace.
  * Debug build: the library compiled with -DDPCLIP_DEBUG (libdpclip_debug.so) checks, before each
  * main-loop store or load of its kernels, that the index lies inside the buffer the host

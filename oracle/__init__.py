@@ -5,3 +5,4 @@ legs may import this package.  The CUDA library never does, and it shares no cod
 """
 from .dp_oracle import *  # noqa: F401,F403
 from .dp_oracle import __all__  # noqa: F401
+from .param_oracle import *  # noqa: F401,F403

@@ -18,6 +18,7 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libdpclip_debug.so")
 (DP_OK, DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_WORKSPACE, DP_ERR_CUDA, DP_ERR_TIMEOUT,
  DP_ERR_DEVICE_CHECK) = range(7)
 DP_F32, DP_BF16 = 0, 1
+DP_I32, DP_I64 = 0, 1
 DP_NORM_AUTO, DP_NORM_GHOST, DP_NORM_EXPLICIT, DP_NORM_ONCE = 0, 1, 2, 3
 METHODS = {"auto": DP_NORM_AUTO, "ghost": DP_NORM_GHOST, "explicit": DP_NORM_EXPLICIT,
            "once": DP_NORM_ONCE}
@@ -75,6 +76,35 @@ SIGNATURES = {
     "dp_projected_adam_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int,
                                         _c_int, _c_int, _c_float, _c_float, _c_float, _c_float, _c_float,
                                         _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    "dp_embedding_lookup": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_float, _c_ll, _c_int, _c_int,
+                                     _c_void_p, _c_int, _c_void_p]),
+    "dp_embedding_workspace_size": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "dp_embedding_per_sample_norms": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                               _c_int, _c_float, _c_ll, _c_void_p, _c_void_p, _c_size_t,
+                                               _c_void_p]),
+    "dp_embedding_clip_accumulate": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                              _c_int, _c_float, _c_ll, _c_void_p, _c_float, _c_void_p,
+                                              _c_void_p, _c_size_t, _c_void_p]),
+    "dp_embedding_step": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                   _c_float, _c_ll, _c_float, _c_float, _c_ull, _c_ull, _c_uint, _c_void_p,
+                                   _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "dp_embedding_step_dev_step": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                            _c_int, _c_float, _c_ll, _c_float, _c_float, _c_ull, _c_void_p,
+                                            _c_uint, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "dp_rmsnorm": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_ll, _c_int, _c_float, _c_void_p,
+                            _c_void_p, _c_void_p]),
+    "dp_rmsnorm_workspace_size": (_c_size_t, [_c_int, _c_int, _c_int, _c_int]),
+    "dp_rmsnorm_backward": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
+                                     _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
+                                     _c_void_p]),
+    "dp_rmsnorm_clip_accumulate": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_int, _c_float, _c_void_p,
+                                            _c_void_p]),
+    "dp_rmsnorm_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                 _c_float, _c_float, _c_float, _c_ull, _c_ull, _c_uint, _c_void_p, _c_void_p,
+                                 _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "dp_rmsnorm_step_dev_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
+                                          _c_int, _c_float, _c_float, _c_float, _c_ull, _c_void_p, _c_uint,
+                                          _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
     "dp_profiling_enable": (_c_int, [_c_int]),
     "dp_profiling_kinds": (_c_int, []),
     "dp_profiling_kind_name": (ctypes.c_char_p, [_c_int]),
@@ -401,3 +431,279 @@ def dp_projected_adam_step(W, R, m, v, P, lr, t, beta1=0.9, beta2=0.999, eps=1e-
                                        int(t), _ptr(workspace), workspace.numel(), _stream(stream)),
           "dp_projected_adam_step")
     return W, m, v
+
+
+# ---------------------------------------------------------------- embedding, RMS norm
+class _Launch:
+    """The stream one call is enqueued on.  Every tensor must be contiguous and on one CUDA
+    device; while the object is entered, that device and the call's stream are current, so that
+    what the binding allocates for the call belongs to that stream."""
+
+    def __init__(self, stream, **tensors):
+        import torch
+
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the first tensor on {dev}")
+        self._ctx = []
+        if dev.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(dev))
+        if stream is not None:
+            self._ctx.append(torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)
+                                               if isinstance(stream, int) else stream))
+
+    def __enter__(self):
+        import torch
+
+        for c in self._ctx:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+        return False
+
+
+def _expect(t, name, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _scratch(workspace, need, device, what):
+    import torch
+
+    if need == 0:
+        raise DPError(DP_ERR_INVALID_ARG, what)
+    return torch.empty(need, dtype=torch.uint8, device=device) if workspace is None else workspace
+
+
+def _ws_bytes(ws):
+    return ws.numel() * ws.element_size()
+
+
+def _index_code(ids):
+    import torch
+
+    if ids.dtype == torch.int64:
+        return DP_I64
+    if ids.dtype == torch.int32:
+        return DP_I32
+    raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
+
+
+def dp_embedding_lookup(W, ids, scale=1.0, out=None, out_dtype=None, stream=None):
+    """scale * W[ids] ([*ids.shape, d]); ids outside the table give rows of zeros."""
+    import torch
+
+    if W.dim() != 2:
+        raise ValueError("W must be [V, d]")
+    V, d = int(W.shape[0]), int(W.shape[1])
+    dtype = out.dtype if out is not None else (out_dtype or W.dtype)
+    shape = (*ids.shape, d)
+    _expect(out, "out", shape, dtype)
+    with _Launch(stream, W=W, ids=ids, out=out) as s:
+        Y = torch.empty(shape, dtype=dtype, device=W.device) if out is None else out
+        if ids.numel():
+            check(lib().dp_embedding_lookup(_ptr(W), _dtype_code(W), _ptr(ids), _index_code(ids), float(scale),
+                                            ids.numel(), V, d, _ptr(Y), _dtype_code(Y), s),
+                  "dp_embedding_lookup")
+    return Y
+
+
+def _embedding_dims(ids, dY):
+    if ids.dim() != 2 or dY.dim() != 3 or tuple(dY.shape[:2]) != tuple(ids.shape):
+        raise ValueError("ids must be [B, T] and dY [B, T, d]")
+    return int(dY.shape[0]), int(dY.shape[1]), int(dY.shape[2])
+
+
+def embedding_workspace_size(B, T, V, d, dtype_code=DP_BF16):
+    return int(lib().dp_embedding_workspace_size(B, T, V, d, dtype_code))
+
+
+def _padding(padding_idx):
+    return -1 if padding_idx is None else int(padding_idx)
+
+
+def dp_embedding_per_sample_norms(ids, dY, V, scale=1.0, padding_idx=None, norms=None, workspace=None, stream=None):
+    """Per-sample norms (fp32 [B]) of the gradient of an embedding table of V rows."""
+    import torch
+
+    B, T, d = _embedding_dims(ids, dY)
+    _expect(norms, "norms", (B,), torch.float32)
+    with _Launch(stream, dY=dY, ids=ids, norms=norms, workspace=workspace) as s:
+        ws = _scratch(workspace, embedding_workspace_size(B, T, int(V), d, _dtype_code(dY)), dY.device,
+                      "dp_embedding_workspace_size")
+        if norms is None:
+            norms = torch.empty(B, dtype=torch.float32, device=dY.device)
+        check(lib().dp_embedding_per_sample_norms(_ptr(ids), _index_code(ids), _ptr(dY), _dtype_code(dY), B, T,
+                                                  int(V), d, float(scale), _padding(padding_idx), _ptr(norms),
+                                                  _ptr(ws), _ws_bytes(ws), s),
+              "dp_embedding_per_sample_norms")
+    return norms
+
+
+def dp_embedding_clip_accumulate(ids, dY, norms, C, G_sum, scale=1.0, padding_idx=None, workspace=None, stream=None):
+    """G_sum[V, d] += sum_i c_i G_i for given norms; rows that no token names are not touched."""
+    import torch
+
+    B, T, d = _embedding_dims(ids, dY)
+    if G_sum.dim() != 2:
+        raise ValueError("G_sum must be [V, d]")
+    V = int(G_sum.shape[0])
+    _expect(G_sum, "G_sum", (V, d), torch.float32)
+    _expect(norms, "norms", (B,), torch.float32)
+    with _Launch(stream, dY=dY, ids=ids, norms=norms, G_sum=G_sum, workspace=workspace) as s:
+        ws = _scratch(workspace, embedding_workspace_size(B, T, V, d, _dtype_code(dY)), dY.device,
+                      "dp_embedding_workspace_size")
+        check(lib().dp_embedding_clip_accumulate(_ptr(ids), _index_code(ids), _ptr(dY), _dtype_code(dY), B, T, V, d,
+                                                 float(scale), _padding(padding_idx), _ptr(norms), float(C),
+                                                 _ptr(G_sum), _ptr(ws), _ws_bytes(ws), s),
+              "dp_embedding_clip_accumulate")
+    return G_sum
+
+
+def dp_embedding_step(ids, dY, V, C, sigma, seed, step, layer_id, scale=1.0, padding_idx=None, norms_out=None,
+                      G_out=None, workspace=None, stream=None):
+    """The privatised gradient of an embedding table of V rows; returns (G_out [V, d], norms_out).
+
+    ``ids`` [B, T] int32 or int64, ``dY`` [B, T, d]; ``step`` as in dp_linear_step.
+    """
+    import torch
+
+    B, T, d = _embedding_dims(ids, dY)
+    V = int(V)
+    _expect(G_out, "G_out", (V, d), torch.float32)
+    _expect(norms_out, "norms_out", (B,), torch.float32)
+    dstep = _device_step(step)
+    with _Launch(stream, dY=dY, ids=ids, norms_out=norms_out, G_out=G_out, workspace=workspace, step=dstep) as s:
+        ws = _scratch(workspace, embedding_workspace_size(B, T, V, d, _dtype_code(dY)), dY.device,
+                      "dp_embedding_workspace_size")
+        if G_out is None:
+            G_out = torch.empty(V, d, dtype=torch.float32, device=dY.device)
+        if norms_out is None:
+            norms_out = torch.empty(B, dtype=torch.float32, device=dY.device)
+        entry = lib().dp_embedding_step if dstep is None else lib().dp_embedding_step_dev_step
+        check(entry(_ptr(ids), _index_code(ids), _ptr(dY), _dtype_code(dY), B, T, V, d, float(scale),
+                    _padding(padding_idx), float(C), float(sigma), int(seed),
+                    int(step) if dstep is None else _ptr(dstep), int(layer_id), _ptr(norms_out), _ptr(G_out),
+                    _ptr(ws), _ws_bytes(ws), s),
+              "dp_embedding_step")
+    return G_out, norms_out
+
+
+def dp_rmsnorm(X, gain, eps=1e-6, residual=None, H_out=None, Y=None, stream=None):
+    """(y, h): h = X + residual (X itself without one), y = h / rms(h) * gain, over the last axis."""
+    import torch
+
+    d = int(X.shape[-1])
+    _expect(gain, "gain", (d,), torch.float32)
+    _expect(residual, "residual", X.shape, X.dtype)
+    _expect(H_out, "H_out", X.shape, X.dtype)
+    _expect(Y, "Y", X.shape, X.dtype)
+    if residual is None and H_out is not None:
+        raise ValueError("H_out needs a residual: without one h is X itself")
+    with _Launch(stream, X=X, gain=gain, residual=residual, H_out=H_out, Y=Y) as s:
+        Y = torch.empty_like(X) if Y is None else Y
+        H = X
+        if residual is not None:
+            H = torch.empty_like(X) if H_out is None else H_out
+        if X.numel():
+            check(lib().dp_rmsnorm(_ptr(X), _ptr(residual), _ptr(gain), _dtype_code(X), X.numel() // d, d, float(eps),
+                                   _ptr(H) if residual is not None else None, _ptr(Y), s), "dp_rmsnorm")
+    return Y, H
+
+
+def rmsnorm_workspace_size(B, T, d, dtype_code=DP_BF16):
+    return int(lib().dp_rmsnorm_workspace_size(B, T, d, dtype_code))
+
+
+def _norm_dims(H, dY, gain, residual_grad, dX):
+    import torch
+
+    if H.dim() != 3:
+        raise ValueError("H must be [B, T, d]")
+    d = int(H.shape[2])
+    _expect(dY, "dY", H.shape, H.dtype)
+    _expect(gain, "gain", (d,), torch.float32)
+    _expect(residual_grad, "residual_grad", H.shape, H.dtype)
+    _expect(dX, "dX", H.shape, H.dtype)
+    return int(H.shape[0]), int(H.shape[1]), d
+
+
+def dp_rmsnorm_backward(H, gain, dY, eps=1e-6, residual_grad=None, dX=None, per_sample=None, norms=None,
+                        workspace=None, stream=None):
+    """(dX, per-sample gain gradients fp32 [B, d], their norms fp32 [B]); nothing is clipped yet."""
+    import torch
+
+    B, T, d = _norm_dims(H, dY, gain, residual_grad, dX)
+    _expect(per_sample, "per_sample", (B, d), torch.float32)
+    _expect(norms, "norms", (B,), torch.float32)
+    with _Launch(stream, H=H, gain=gain, dY=dY, residual_grad=residual_grad, dX=dX, per_sample=per_sample,
+                 norms=norms, workspace=workspace) as s:
+        ws = _scratch(workspace, rmsnorm_workspace_size(B, T, d, _dtype_code(H)), H.device,
+                      "dp_rmsnorm_workspace_size")
+        dX = torch.empty_like(H) if dX is None else dX
+        if per_sample is None:
+            per_sample = torch.empty(B, d, dtype=torch.float32, device=H.device)
+        if norms is None:
+            norms = torch.empty(B, dtype=torch.float32, device=H.device)
+        check(lib().dp_rmsnorm_backward(_ptr(H), _ptr(gain), _ptr(dY), _ptr(residual_grad), _dtype_code(H), B, T, d,
+                                        float(eps), _ptr(dX), _ptr(per_sample), _ptr(norms), _ptr(ws), _ws_bytes(ws),
+                                        s), "dp_rmsnorm_backward")
+    return dX, per_sample, norms
+
+
+def dp_rmsnorm_clip_accumulate(per_sample, norms, C, G_sum, stream=None):
+    """G_sum[d] += sum_i min(1, C / norms[i]) per_sample[i]."""
+    import torch
+
+    if per_sample.dim() != 2:
+        raise ValueError("per_sample must be [B, d]")
+    B, d = int(per_sample.shape[0]), int(per_sample.shape[1])
+    _expect(per_sample, "per_sample", (B, d), torch.float32)
+    _expect(norms, "norms", (B,), torch.float32)
+    _expect(G_sum, "G_sum", (d,), torch.float32)
+    with _Launch(stream, per_sample=per_sample, norms=norms, G_sum=G_sum) as s:
+        check(lib().dp_rmsnorm_clip_accumulate(_ptr(per_sample), _ptr(norms), B, d, float(C), _ptr(G_sum), s),
+              "dp_rmsnorm_clip_accumulate")
+    return G_sum
+
+
+def dp_rmsnorm_step(H, gain, dY, C, sigma, seed, step, layer_id, eps=1e-6, residual_grad=None, dX=None,
+                    norms_out=None, G_out=None, workspace=None, stream=None):
+    """The backward of dp_rmsnorm with the gain's privatised gradient: (dX, G_out [d], norms_out).
+
+    ``H`` is the h of the forward, ``residual_grad`` the gradient that reaches h past the norm;
+    ``step`` as in dp_linear_step.
+    """
+    import torch
+
+    B, T, d = _norm_dims(H, dY, gain, residual_grad, dX)
+    _expect(G_out, "G_out", (d,), torch.float32)
+    _expect(norms_out, "norms_out", (B,), torch.float32)
+    dstep = _device_step(step)
+    with _Launch(stream, H=H, gain=gain, dY=dY, residual_grad=residual_grad, dX=dX, norms_out=norms_out, G_out=G_out,
+                 workspace=workspace, step=dstep) as s:
+        ws = _scratch(workspace, rmsnorm_workspace_size(B, T, d, _dtype_code(H)), H.device,
+                      "dp_rmsnorm_workspace_size")
+        dX = torch.empty_like(H) if dX is None else dX
+        if G_out is None:
+            G_out = torch.empty(d, dtype=torch.float32, device=H.device)
+        if norms_out is None:
+            norms_out = torch.empty(B, dtype=torch.float32, device=H.device)
+        entry = lib().dp_rmsnorm_step if dstep is None else lib().dp_rmsnorm_step_dev_step
+        check(entry(_ptr(H), _ptr(gain), _ptr(dY), _ptr(residual_grad), _dtype_code(H), B, T, d, float(eps), float(C),
+                    float(sigma), int(seed), int(step) if dstep is None else _ptr(dstep), int(layer_id), _ptr(dX),
+                    _ptr(norms_out), _ptr(G_out), _ptr(ws), _ws_bytes(ws), s),
+              "dp_rmsnorm_step")
+    return dX, G_out, norms_out

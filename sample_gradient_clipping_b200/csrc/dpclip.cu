@@ -17,8 +17,10 @@
 #include <vector>
 
 #include "dpclip.h"
+#include "embedding.cuh"
 #include "launch_profiler.h"
 #include "nvtx_range.h"
+#include "rmsnorm.cuh"
 #include "rng.cuh"
 #include "simt.cuh"
 #include "umma_gemm.cuh"
@@ -2312,6 +2314,7 @@ dp_status dp_workspace_status(const void* workspace, void* stream) {
     snprintf(g_cuda_error, sizeof(g_cuda_error), "device-side check %u failed", word - kDebugCheckBase);
     return DP_ERR_DEVICE_CHECK;
   }
+  if (word == kStatusIdRange) return DP_ERR_INVALID_ARG;  // a token id at or past the table's end
   return word ? DP_ERR_TIMEOUT : DP_OK;
 }
 
@@ -2375,3 +2378,6 @@ dp_status dp_profiling_collect(double* total_ms, long long* launches) {
 long long dp_kernel_launches(void) { return profiler().launches.load(); }
 
 }  // extern "C"
+
+#include "embedding_host.cuh"
+#include "rmsnorm_host.cuh"

@@ -32,6 +32,13 @@ enum KernelKind : int {
   kKindAxpy,          // tcgen05 W += alpha U P^T
   kKindGhostShared,   // tcgen05 one X Gram shared by the dY Grams of up to three linears
   kKindCombine,       // the split partials of clipped sums split over K, added in split order
+  kKindEmbLookup,     // scaled rows of the embedding table
+  kKindEmbSort,       // the tokens sorted by id, and their groups
+  kKindEmbNorm,       // squared group sums of the table's per-sample gradients
+  kKindEmbSum,        // the table's clipped sum + noise
+  kKindRmsNorm,       // RMS norm with the residual's addition
+  kKindRmsNormBackward,  // its backward, with the gain gradient's partial sums
+  kKindRmsNormGain,   // the gain's per-sample gradients and their clipped sum + noise
   kNumKinds
 };
 
@@ -40,7 +47,8 @@ inline const char* kernel_kind_name(int k) {
       "noise_add",  "projection",   "philox_blocks", "scale_rows_bf16", "finalize_norms",
       "f32_norm",   "f32_clipsum",  "f32_project",   "umma_clipsum",    "umma_explicit_norm",
       "umma_ghost_norm", "umma_project", "umma_explicit_store", "clip_reduce", "adam_rspace",
-      "umma_axpy", "umma_ghost_shared", "split_combine"};
+      "umma_axpy", "umma_ghost_shared", "split_combine", "embedding_lookup", "embedding_sort", "embedding_norm",
+      "embedding_sum", "rmsnorm", "rmsnorm_backward", "rmsnorm_gain"};
   return (k >= 0 && k < kNumKinds) ? names[k] : "";
 }
 

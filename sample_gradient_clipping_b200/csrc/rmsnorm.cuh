@@ -1,0 +1,311 @@
+// RMS norm with the residual's addition, its backward, and the privatised gradient of its gain.
+//
+//   h = round(x + res),  r = 1 / sqrt(mean_j h_j^2 + eps),  y_j = h_j r g_j;
+//   backward, u_j = g_j dy_j:  dh_j = r u_j - h_j r^3 mean_k(u_k h_k)  (+ the gradient that
+//   reaches h past the norm);
+//   sample i's gain gradient  g_i[j] = sum_t dy_tj h_tj r_t,  n_i = ||g_i||,
+//   S[j] = sum_i c_i g_i[j] + sigma C z_j.
+// r is formed again in the backward from the row it reads anyway, so nothing but h is kept.
+// Every sum of a row or a column is in fp32, the sums over samples and norms in fp64, all in a
+// fixed order: the bits repeat.
+//
+// A row is held by kTpr threads, kNv vectors of 16 bytes each, so it is read once: its two sums
+// (h^2 and u h) are one reduction.  Columns stay with their thread, so the gain's values and the
+// gain gradient's sums live in registers across the rows of a block.  Both kernels are bound by
+// HBM.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "embedding.cuh"
+#include "ptx.cuh"
+#include "rng.cuh"
+#include "simt.cuh"
+
+namespace dpclip {
+
+template <typename T, int V>
+__device__ __forceinline__ uint4 pack16(const float (&f)[V], const T*) {
+  uint4 q;
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+  } else {
+    q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  return q;
+}
+
+// Sums a and b over the kTpr threads of a row.  More than a warp: through shared memory, two
+// slots in turn so that one barrier a row is enough (a slot is written again only after every
+// thread has passed the barrier of the row between).
+template <int kTpr>
+__device__ __forceinline__ void row_sums(float& a, float& b, float (*red)[2][kTpr / 32 > 0 ? kTpr / 32 : 1], int turn) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (kTpr > 32) {
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x % 32 == 0) {
+      red[turn][0][warp] = a;
+      red[turn][1][warp] = b;
+    }
+    __syncthreads();
+    a = 0.0f;
+    b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kTpr / 32; ++w) {
+      a += red[turn][0][w];
+      b += red[turn][1][w];
+    }
+  }
+}
+
+// One row per kTpr threads; a block of kThreads threads takes kThreads / kTpr rows at a time.
+template <typename T, int kTpr, int kNv, bool RES>
+__global__ void __launch_bounds__(kTpr < 128 ? 128 : kTpr)
+    rmsnorm_kernel(const T* __restrict__ X, const T* __restrict__ res, const float* __restrict__ gain, long long rows,
+                   int d, float eps, T* __restrict__ H, T* __restrict__ Y) {
+  griddep_enter();
+  constexpr int V = EmbVec<T>::N;
+  constexpr int kThreads = kTpr < 128 ? 128 : kTpr;
+  constexpr int kRows = kThreads / kTpr;
+  __shared__ float red[2][2][kTpr / 32 > 0 ? kTpr / 32 : 1];
+  const int t = threadIdx.x % kTpr;
+  const int vecs = d / V;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  int turn = 0;
+  // kRows > 1 only with a warp per row: no barrier then, so warps may run out of rows alone.
+  for (long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kTpr; row < rows;
+       row += static_cast<long long>(gridDim.x) * kRows, turn ^= 1) {
+    const uint4* x = reinterpret_cast<const uint4*>(X + row * d);
+    const uint4* r = RES ? reinterpret_cast<const uint4*>(res + row * d) : nullptr;
+    uint4 q[kNv], qr[kNv];
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      q[k] = qr[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (t + k * kTpr < vecs) {
+        q[k] = __ldg(x + t + k * kTpr);
+        if constexpr (RES) qr[k] = __ldg(r + t + k * kTpr);
+      }
+    }
+    float ss = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      float f[V];
+      unpack16(q[k], f, X);
+      if constexpr (RES) {
+        float e[V];
+        unpack16(qr[k], e, X);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] += e[j];
+        q[k] = pack16<T, V>(f, X);  // h as its backward will read it; the norm is of that
+        unpack16(q[k], f, X);
+        if (t + k * kTpr < vecs) reinterpret_cast<uint4*>(H + row * d)[t + k * kTpr] = q[k];
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(f[j], f[j], ss);
+    }
+    row_sums<kTpr>(ss, none, red, turn);
+    const float inv = 1.0f / sqrtf(fmaf(ss, inv_d, eps));
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      if (t + k * kTpr >= vecs) continue;
+      float f[V];
+      unpack16(q[k], f, X);
+      const float4* g = reinterpret_cast<const float4*>(gain + static_cast<long long>(t + k * kTpr) * V);
+#pragma unroll
+      for (int e = 0; e < V / 4; ++e) {
+        const float4 w = __ldg(g + e);
+        f[4 * e] = f[4 * e] * inv * w.x;
+        f[4 * e + 1] = f[4 * e + 1] * inv * w.y;
+        f[4 * e + 2] = f[4 * e + 2] * inv * w.z;
+        f[4 * e + 3] = f[4 * e + 3] * inv * w.w;
+      }
+      if (!DP_DCHECK(in_buffer(row * d + static_cast<long long>(t + k * kTpr) * V, V, rows * d), 50u, nullptr)) continue;
+      reinterpret_cast<uint4*>(Y + row * d)[t + k * kTpr] = pack16<T, V>(f, X);
+    }
+  }
+}
+
+// Block (part, sample): rows [part per, part per + per) of the sample.  Writes dh and the block's
+// column sums of dy h r into parts[sample][part][d].
+template <typename T, int kTpr, int kNv, bool RES>
+__global__ void __launch_bounds__(kTpr)
+    rmsnorm_backward_kernel(const T* __restrict__ H, const float* __restrict__ gain, const T* __restrict__ dY,
+                            const T* __restrict__ dres, int T_len, int d, float eps, int per, T* __restrict__ dX,
+                            float* __restrict__ parts, uint32_t* __restrict__ status) {
+  griddep_enter();
+  constexpr int V = EmbVec<T>::N;
+  __shared__ float red[2][2][kTpr / 32 > 0 ? kTpr / 32 : 1];
+  const int t = threadIdx.x;
+  const int vecs = d / V;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) *status = 0u;
+  float g[kNv][V], acc[kNv][V];
+#pragma unroll
+  for (int k = 0; k < kNv; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      g[k][j] = t + k * kTpr < vecs ? __ldg(gain + (t + k * kTpr) * V + j) : 0.0f;
+      acc[k][j] = 0.0f;
+    }
+  const int first = blockIdx.x * per;
+  const int last = min(T_len, first + per);
+  int turn = 0;
+  for (int s = first; s < last; ++s, turn ^= 1) {
+    const long long at = (static_cast<long long>(blockIdx.y) * T_len + s) * d;
+    uint4 qh[kNv], qy[kNv], qr[kNv];
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      qh[k] = qy[k] = qr[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (t + k * kTpr < vecs) {
+        qh[k] = __ldg(reinterpret_cast<const uint4*>(H + at) + t + k * kTpr);
+        qy[k] = __ldg(reinterpret_cast<const uint4*>(dY + at) + t + k * kTpr);
+        if constexpr (RES) qr[k] = __ldg(reinterpret_cast<const uint4*>(dres + at) + t + k * kTpr);
+      }
+    }
+    float hh = 0.0f, uh = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      float h[V], y[V];
+      unpack16(qh[k], h, H);
+      unpack16(qy[k], y, H);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        hh = fmaf(h[j], h[j], hh);
+        uh = fmaf(y[j] * g[k][j], h[j], uh);
+      }
+    }
+    row_sums<kTpr>(hh, uh, red, turn);
+    const float inv = 1.0f / sqrtf(fmaf(hh, inv_d, eps));
+    const float w = inv * inv * inv * (uh * inv_d);
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      float h[V], y[V], o[V];
+      unpack16(qh[k], h, H);
+      unpack16(qy[k], y, H);
+      if constexpr (RES) unpack16(qr[k], o, H);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        acc[k][j] = fmaf(y[j], h[j] * inv, acc[k][j]);
+        const float dh = fmaf(inv, y[j] * g[k][j], -(h[j] * w));
+        o[j] = RES ? o[j] + dh : dh;
+      }
+      if (t + k * kTpr < vecs && DP_DCHECK(s < T_len, 51u, status))
+        reinterpret_cast<uint4*>(dX + at)[t + k * kTpr] = pack16<T, V>(o, H);
+    }
+  }
+  float* out = parts + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * d;
+#pragma unroll
+  for (int k = 0; k < kNv; ++k) {
+    if (t + k * kTpr >= vecs) continue;
+#pragma unroll
+    for (int e = 0; e < V / 4; ++e)
+      reinterpret_cast<float4*>(out + (t + k * kTpr) * V)[e] =
+          make_float4(acc[k][4 * e], acc[k][4 * e + 1], acc[k][4 * e + 2], acc[k][4 * e + 3]);
+  }
+}
+
+constexpr int kGainThreads = 256;
+
+// per_sample[i][j] = sum over the sample's parts, in part order, and the block's share of n_i^2
+// into sq[i][blockIdx.x].  blockIdx.y: sample.
+__global__ void __launch_bounds__(kGainThreads)
+    rmsnorm_gain_kernel(const float* __restrict__ parts, int nparts, int d, float* __restrict__ per_sample,
+                        float* __restrict__ sq) {
+  griddep_enter();
+  __shared__ float part[kGainThreads / 32];
+  const int j = blockIdx.x * kGainThreads + threadIdx.x;
+  const long long i = blockIdx.y;
+  double sum = 0.0;
+  if (j < d) {
+    const float* p = parts + i * nparts * d + j;
+#pragma unroll 8
+    for (int k = 0; k < nparts; ++k) sum += static_cast<double>(p[static_cast<long long>(k) * d]);
+    per_sample[i * d + j] = static_cast<float>(sum);
+  }
+  const float f = static_cast<float>(sum);
+  const float ss = warp_sum(f * f);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = ss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int w = 0; w < kGainThreads / 32; ++w) s += part[w];
+    sq[i * gridDim.x + blockIdx.x] = s;
+  }
+}
+
+// norms[i] = sqrt(sum of the sample's `blocks` shares), one warp per sample.
+__global__ void rmsnorm_norms_kernel(const float* __restrict__ sq, int blocks, int B, float* __restrict__ norms) {
+  griddep_enter();
+  const int i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  if (i >= B) return;
+  const float n2 = warp_norm2_from_partials(sq, blocks, blocks, i, threadIdx.x % 32);
+  if (threadIdx.x % 32 == 0) norms[i] = sqrtf(n2);
+}
+
+// S[j] (+)= sum_i c_i per_sample[i][j] + std z_j, four columns a thread.  The norms are given, or
+// (sq non-null) formed from the shares by each block; block 0 then writes norms_out.
+constexpr int kGainSamples = 1024;  // clip factors held at a time
+constexpr int kGainSumThreads = 128;
+__global__ void __launch_bounds__(kGainSumThreads)
+    rmsnorm_sum_kernel(const float* __restrict__ per_sample, const float* __restrict__ norms,
+                       const float* __restrict__ sq, int sq_blocks, int B, int d, float C, int accumulate,
+                       double noise_std, PhiloxKey key, uint32_t layer_id, StepRef step, float* __restrict__ norms_out,
+                       float* __restrict__ S, uint32_t* __restrict__ status) {
+  griddep_enter();
+  __shared__ float c[kGainSamples];
+  __shared__ double acc_s[kGainSumThreads][4];
+  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // 32 groups of 4 columns a block; the 4 warps share the samples, in a fixed split.
+  const int j = (blockIdx.x * 32 + lane) * 4;
+  double a[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int base = 0; base < B; base += kGainSamples) {
+    const int count = min(kGainSamples, B - base);
+    __syncthreads();
+    if (sq) {
+      for (int i = warp; i < count; i += kGainSumThreads / 32) {
+        const float n = sqrtf(warp_norm2_from_partials(sq, sq_blocks, sq_blocks, base + i, lane));
+        if (lane == 0) {
+          c[i] = clip_factor(n, C);
+          if (blockIdx.x == 0 && norms_out) norms_out[base + i] = n;
+        }
+      }
+    } else {
+      for (int i = threadIdx.x; i < count; i += kGainSumThreads) c[i] = clip_factor(norms[base + i], C);
+    }
+    __syncthreads();
+    if (j < d) {
+#pragma unroll 4
+      for (int i = warp; i < count; i += kGainSumThreads / 32) {
+        const float4 x = *reinterpret_cast<const float4*>(per_sample + static_cast<long long>(base + i) * d + j);
+        const double w = static_cast<double>(c[i]);
+        a[0] = fma(w, static_cast<double>(x.x), a[0]);
+        a[1] = fma(w, static_cast<double>(x.y), a[1]);
+        a[2] = fma(w, static_cast<double>(x.z), a[2]);
+        a[3] = fma(w, static_cast<double>(x.w), a[3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc_s[threadIdx.x][e] = a[e];
+  __syncthreads();
+  if (warp != 0 || j >= d) return;
+  double z[4] = {0.0, 0.0, 0.0, 0.0};
+  if (noise_std != 0.0)
+    normals4(static_cast<uint32_t>(j / 4), layer_id, step.get(), kStreamNoise, key, z, NoiseTablesGlobal{}, noise_std);
+  float4 o = accumulate ? *reinterpret_cast<const float4*>(S + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float* of = &o.x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    double s = 0.0;
+    for (int w = 0; w < kGainSumThreads / 32; ++w) s += acc_s[w * 32 + lane][e];
+    of[e] = static_cast<float>(static_cast<double>(of[e]) + s + z[e]);
+  }
+  if (DP_DCHECK(j + 4 <= d, 52u, status)) *reinterpret_cast<float4*>(S + j) = o;
+}
+
+}  // namespace dpclip

@@ -1,0 +1,243 @@
+// Host side of the RMS norm entry points: checks, workspace layout and launches.  Included by
+// dpclip.cu after its launch helpers.
+#pragma once
+
+namespace {
+
+struct NormCall {
+  int B, T, d;
+  dp_dtype dt;
+  long long N() const { return static_cast<long long>(B) * T; }
+  int vecs() const { return d / (dt == DP_BF16 ? 8 : 4); }
+};
+
+// A row is at most 2048 vectors of 16 bytes: 512 threads hold four each.
+constexpr int kNormMaxVecs = 2048;
+
+dp_status check_norm_shape(const NormCall& s) {
+  if (!valid_dtype(s.dt) || s.B < 1 || s.T < 1 || s.d < 1 || s.d % (s.dt == DP_BF16 ? 8 : 4)) return DP_ERR_INVALID_ARG;
+  if (s.N() >= (1ll << 31) || s.B > 65535) return DP_ERR_INVALID_ARG;
+  return s.vecs() > kNormMaxVecs ? DP_ERR_UNSUPPORTED : DP_OK;
+}
+
+// Threads of a row in the backward, and how many blocks of that size it is cut for on 148 SMs.
+int norm_row_threads(const NormCall& s) {
+  const int v = s.vecs();
+  return v <= 128 ? 32 : v <= 512 ? 128 : v <= 1024 ? 256 : 512;
+}
+
+// Parts of a sample in the backward: blocks fill 148 SMs, each part a run of rows.
+int norm_parts(const NormCall& s) {
+  const int tpr = norm_row_threads(s);
+  const int per_sm = tpr == 32 ? 16 : tpr == 128 ? 4 : tpr == 256 ? 2 : 1;
+  const long long want = std::max(1, 148 * per_sm / s.B);
+  const int per = static_cast<int>((s.T + want - 1) / want);
+  return ceil_div(s.T, per);
+}
+
+struct NormLayout {
+  size_t parts, per_sample, sq, total;
+};
+
+NormLayout norm_layout(const NormCall& s) {
+  NormLayout L;
+  L.parts = 256;
+  L.per_sample = L.parts + align256(static_cast<size_t>(s.B) * norm_parts(s) * s.d * 4);
+  L.sq = L.per_sample + align256(static_cast<size_t>(s.B) * s.d * 4);
+  L.total = L.sq + align256(static_cast<size_t>(s.B) * ceil_div(s.d, kGainThreads) * 4);
+  return L;
+}
+
+template <typename T, int TPR, int NV>
+dp_status rmsnorm_launch(const NormCall& s, long long rows, const void* X, const void* res, const float* gain, float eps,
+                         void* H, void* Y, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR;
+  const long long blocks = (rows + threads / TPR - 1) / (threads / TPR);
+  const long long cap = static_cast<long long>(sm_count()) * (2048 / threads) * 4;
+  const unsigned grid = static_cast<unsigned>(std::min(blocks, cap));
+  LaunchScope scope(kKindRmsNorm, stream);
+  if (res) {
+    DP_LAUNCH("rmsnorm_kernel", (rmsnorm_kernel<T, TPR, NV, true>), grid, threads, 0, stream, static_cast<const T*>(X),
+              static_cast<const T*>(res), gain, rows, s.d, eps, static_cast<T*>(H), static_cast<T*>(Y));
+  } else {
+    DP_LAUNCH("rmsnorm_kernel", (rmsnorm_kernel<T, TPR, NV, false>), grid, threads, 0, stream, static_cast<const T*>(X),
+              static_cast<const T*>(res), gain, rows, s.d, eps, static_cast<T*>(H), static_cast<T*>(Y));
+  }
+  return DP_OK;
+}
+
+template <typename T>
+dp_status rmsnorm_as(const NormCall& s, long long rows, const void* X, const void* res, const float* gain, float eps,
+                     void* H, void* Y, cudaStream_t stream) {
+  const int v = s.vecs();
+  if (v <= 32) return rmsnorm_launch<T, 32, 1>(s, rows, X, res, gain, eps, H, Y, stream);
+  if (v <= 128) return rmsnorm_launch<T, 32, 4>(s, rows, X, res, gain, eps, H, Y, stream);
+  if (v <= 256) return rmsnorm_launch<T, 128, 2>(s, rows, X, res, gain, eps, H, Y, stream);
+  if (v <= 512) return rmsnorm_launch<T, 128, 4>(s, rows, X, res, gain, eps, H, Y, stream);
+  if (v <= 1024) return rmsnorm_launch<T, 256, 4>(s, rows, X, res, gain, eps, H, Y, stream);
+  return rmsnorm_launch<T, 512, 4>(s, rows, X, res, gain, eps, H, Y, stream);
+}
+
+template <typename T, int TPR, int NV>
+dp_status rmsnorm_backward_launch(const NormCall& s, const void* H, const float* gain, const void* dY, const void* dres,
+                                  float eps, void* dX, float* parts, uint32_t* status, cudaStream_t stream) {
+  const int nparts = norm_parts(s);
+  const int per = ceil_div(s.T, nparts);
+  const dim3 grid(static_cast<unsigned>(nparts), static_cast<unsigned>(s.B));
+  LaunchScope scope(kKindRmsNormBackward, stream);
+  if (dres) {
+    DP_LAUNCH("rmsnorm_backward_kernel", (rmsnorm_backward_kernel<T, TPR, NV, true>), grid, TPR, 0, stream,
+              static_cast<const T*>(H), gain, static_cast<const T*>(dY), static_cast<const T*>(dres), s.T, s.d, eps, per,
+              static_cast<T*>(dX), parts, status);
+  } else {
+    DP_LAUNCH("rmsnorm_backward_kernel", (rmsnorm_backward_kernel<T, TPR, NV, false>), grid, TPR, 0, stream,
+              static_cast<const T*>(H), gain, static_cast<const T*>(dY), static_cast<const T*>(dres), s.T, s.d, eps, per,
+              static_cast<T*>(dX), parts, status);
+  }
+  return DP_OK;
+}
+
+template <typename T>
+dp_status rmsnorm_backward_as(const NormCall& s, const void* H, const float* gain, const void* dY, const void* dres,
+                              float eps, void* dX, float* parts, uint32_t* status, cudaStream_t stream) {
+  const int v = s.vecs();
+  if (v <= 32) return rmsnorm_backward_launch<T, 32, 1>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  if (v <= 128) return rmsnorm_backward_launch<T, 32, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  if (v <= 256) return rmsnorm_backward_launch<T, 128, 2>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  if (v <= 512) return rmsnorm_backward_launch<T, 128, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  if (v <= 1024) return rmsnorm_backward_launch<T, 256, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  return rmsnorm_backward_launch<T, 512, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+}
+
+dp_status check_norm_backward(const NormCall& s, const void* H, const float* gain, const void* dY, const void* dres,
+                              float eps, const void* dX, const void* workspace, size_t ws_bytes, NormLayout* L) {
+  if (!H || !gain || !dY || !dX || !workspace) return DP_ERR_INVALID_ARG;
+  if (!aligned16(H) || !aligned16(gain) || !aligned16(dY) || !aligned16(dX) || (dres && !aligned16(dres)))
+    return DP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DP_ERR_INVALID_ARG;
+  if (dX == H || dX == dY || dX == dres) return DP_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return DP_ERR_INVALID_ARG;
+  const dp_status st = check_norm_shape(s);
+  if (st != DP_OK) return st;
+  *L = norm_layout(s);
+  return ws_bytes < L->total ? DP_ERR_WORKSPACE : DP_OK;
+}
+
+// dh, and every sample's gain gradient with its squared norm's shares.
+dp_status norm_backward(const NormCall& s, const NormLayout& L, const void* H, const float* gain, const void* dY,
+                        const void* dres, float eps, void* dX, float* per_sample, uint8_t* ws, cudaStream_t stream) {
+  float* parts = reinterpret_cast<float*>(ws + L.parts);
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws);
+  const dp_status st =
+      s.dt == DP_BF16 ? rmsnorm_backward_as<__nv_bfloat16>(s, H, gain, dY, dres, eps, dX, parts, status, stream)
+                      : rmsnorm_backward_as<float>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  if (st != DP_OK) return st;
+  const dim3 grid(static_cast<unsigned>(ceil_div(s.d, kGainThreads)), static_cast<unsigned>(s.B));
+  LaunchScope scope(kKindRmsNormGain, stream);
+  DP_LAUNCH("rmsnorm_gain_kernel", rmsnorm_gain_kernel, grid, kGainThreads, 0, stream, parts, norm_parts(s), s.d,
+            per_sample, reinterpret_cast<float*>(ws + L.sq));
+  return DP_OK;
+}
+
+dp_status norm_sum(int B, int d, const float* per_sample, const float* norms, const float* sq, float C, bool accumulate,
+                   double noise_std, unsigned long long seed, StepRef step, unsigned layer_id, float* norms_out,
+                   float* S, uint32_t* status, cudaStream_t stream) {
+  LaunchScope scope(kKindRmsNormGain, stream);
+  DP_LAUNCH("rmsnorm_sum_kernel", rmsnorm_sum_kernel, ceil_div(d, 128), kGainSumThreads, 0, stream, per_sample, norms, sq,
+            ceil_div(d, kGainThreads), B, d, C, accumulate ? 1 : 0, noise_std, philox_key_from_seed(seed), layer_id, step,
+            norms_out, S, status);
+  return DP_OK;
+}
+
+dp_status rmsnorm_step(const void* H, const float* gain, const void* dY, const void* dres, dp_dtype dt, int B, int T,
+                       int d, float eps, float C, float sigma, unsigned long long seed, StepRef step, unsigned layer_id,
+                       void* dX, float* norms_out, float* G_out, void* workspace, size_t ws_bytes, void* stream) {
+  const NormCall s{B, T, d, dt};
+  NormLayout L;
+  dp_status st = check_norm_backward(s, H, gain, dY, dres, eps, dX, workspace, ws_bytes, &L);
+  if (st != DP_OK) return st;
+  if (!G_out || !aligned16(G_out)) return DP_ERR_INVALID_ARG;
+  if (!(C > 0.0f) || !(sigma >= 0.0f) || std::isinf(sigma)) return DP_ERR_INVALID_ARG;
+  if (std::isinf(C) && sigma != 0.0f) return DP_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  float* per_sample = reinterpret_cast<float*>(ws + L.per_sample);
+  if ((st = norm_backward(s, L, H, gain, dY, dres, eps, dX, per_sample, ws, cs)) != DP_OK) return st;
+  const double noise_std = (sigma == 0.0f) ? 0.0 : static_cast<double>(sigma) * static_cast<double>(C);
+  return norm_sum(B, d, per_sample, nullptr, reinterpret_cast<float*>(ws + L.sq), C, false, noise_std, seed, step,
+                  layer_id, norms_out, G_out, nullptr, cs);
+}
+
+}  // namespace
+
+extern "C" {
+
+dp_status dp_rmsnorm(const void* X, const void* residual, const float* gain, dp_dtype dt, long long rows, int d,
+                     float eps, void* H, void* Y, void* stream) {
+  DP_NVTX_RANGE();
+  if (!X || !gain || !Y || (residual && !H)) return DP_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(gain) || !aligned16(Y) || (residual && (!aligned16(residual) || !aligned16(H))))
+    return DP_ERR_INVALID_ARG;
+  if (Y == X || Y == residual || (residual && (H == X || H == residual || H == Y))) return DP_ERR_INVALID_ARG;
+  if (rows < 1 || rows >= (1ll << 31) || !(eps >= 0.0f) || std::isinf(eps)) return DP_ERR_INVALID_ARG;
+  const NormCall s{1, 1, d, dt};
+  const dp_status st = check_norm_shape(s);
+  if (st != DP_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return dt == DP_BF16 ? rmsnorm_as<__nv_bfloat16>(s, rows, X, residual, gain, eps, H, Y, cs)
+                       : rmsnorm_as<float>(s, rows, X, residual, gain, eps, H, Y, cs);
+}
+
+size_t dp_rmsnorm_workspace_size(int B, int T, int d, dp_dtype dt) {
+  const NormCall s{B, T, d, dt};
+  return check_norm_shape(s) == DP_OK ? norm_layout(s).total : 0;
+}
+
+dp_status dp_rmsnorm_backward(const void* H, const float* gain, const void* dY, const void* residual_grad, dp_dtype dt,
+                              int B, int T, int d, float eps, void* dX, float* per_sample, float* norms,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  DP_NVTX_RANGE();
+  const NormCall s{B, T, d, dt};
+  NormLayout L;
+  dp_status st = check_norm_backward(s, H, gain, dY, residual_grad, eps, dX, workspace, ws_bytes, &L);
+  if (st != DP_OK) return st;
+  if (!per_sample || !norms || !aligned16(per_sample)) return DP_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if ((st = norm_backward(s, L, H, gain, dY, residual_grad, eps, dX, per_sample, ws, cs)) != DP_OK) return st;
+  LaunchScope scope(kKindFinalize, cs);
+  DP_LAUNCH("rmsnorm_norms_kernel", rmsnorm_norms_kernel, ceil_div(B, 8), 256, 0, cs,
+            reinterpret_cast<float*>(ws + L.sq), ceil_div(d, kGainThreads), B, norms);
+  return DP_OK;
+}
+
+dp_status dp_rmsnorm_clip_accumulate(const float* per_sample, const float* norms, int B, int d, float C, float* G_sum,
+                                     void* stream) {
+  DP_NVTX_RANGE();
+  if (!per_sample || !norms || !G_sum || !aligned16(per_sample) || !aligned16(G_sum)) return DP_ERR_INVALID_ARG;
+  if (B < 1 || d < 1 || d % 4 || !(C > 0.0f)) return DP_ERR_INVALID_ARG;
+  return norm_sum(B, d, per_sample, norms, nullptr, C, true, 0.0, 0, step_value(0), 0, nullptr, G_sum, nullptr,
+                  static_cast<cudaStream_t>(stream));
+}
+
+dp_status dp_rmsnorm_step(const void* H, const float* gain, const void* dY, const void* residual_grad, dp_dtype dt,
+                          int B, int T, int d, float eps, float C, float sigma, unsigned long long seed,
+                          unsigned long long step, unsigned layer_id, void* dX, float* norms_out, float* G_out,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  DP_NVTX_RANGE();
+  return rmsnorm_step(H, gain, dY, residual_grad, dt, B, T, d, eps, C, sigma, seed, step_value(step), layer_id, dX,
+                      norms_out, G_out, workspace, ws_bytes, stream);
+}
+
+dp_status dp_rmsnorm_step_dev_step(const void* H, const float* gain, const void* dY, const void* residual_grad,
+                                   dp_dtype dt, int B, int T, int d, float eps, float C, float sigma,
+                                   unsigned long long seed, const unsigned long long* step_dev, unsigned layer_id,
+                                   void* dX, float* norms_out, float* G_out, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  DP_NVTX_RANGE();
+  if (!step_dev || (reinterpret_cast<uintptr_t>(step_dev) & 7u) != 0) return DP_ERR_INVALID_ARG;
+  return rmsnorm_step(H, gain, dY, residual_grad, dt, B, T, d, eps, C, sigma, seed, StepRef{0u, step_dev}, layer_id, dX,
+                      norms_out, G_out, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"
