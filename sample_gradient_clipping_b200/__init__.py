@@ -6,8 +6,9 @@ synthetic workloads (``inputs``).
 """
 from ._lib import (  # noqa: F401
     DPError, auto_norm_method, dp_add_noise, dp_block_step, dp_clip_accumulate, dp_embedding_clip_accumulate,
-    dp_embedding_lookup, dp_embedding_per_sample_norms, dp_embedding_step, dp_linear_step, dp_philox_blocks,
+    dp_embedding_lookup, dp_embedding_per_sample_norms, dp_embedding_step, dp_linear_step, dp_muon_step, dp_orthogonalize,
+    dp_philox_blocks,
     dp_projected_adam_step, dp_rmsnorm, dp_rmsnorm_backward, dp_rmsnorm_clip_accumulate, dp_rmsnorm_step,
     dp_per_sample_norms, dp_projection_matrix, dp_workspace_status, embedding_workspace_size, lib,
-    rmsnorm_workspace_size, workspace_size,
+    muon_workspace_size, rmsnorm_workspace_size, workspace_size,
 )

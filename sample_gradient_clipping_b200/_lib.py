@@ -105,6 +105,11 @@ SIGNATURES = {
     "dp_rmsnorm_step_dev_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
                                           _c_int, _c_float, _c_float, _c_float, _c_ull, _c_void_p, _c_uint,
                                           _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "dp_muon_workspace_size": (_c_size_t, [_c_int, _c_int]),
+    "dp_orthogonalize": (_c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_size_t,
+                                  _c_void_p]),
+    "dp_muon_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_float, _c_float, _c_int, _c_float,
+                              _c_float, _c_float, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "dp_profiling_enable": (_c_int, [_c_int]),
     "dp_profiling_kinds": (_c_int, []),
     "dp_profiling_kind_name": (ctypes.c_char_p, [_c_int]),
@@ -433,7 +438,7 @@ def dp_projected_adam_step(W, R, m, v, P, lr, t, beta1=0.9, beta2=0.999, eps=1e-
     return W, m, v
 
 
-# ---------------------------------------------------------------- embedding, RMS norm
+# ---------------------------------------------------------------- embedding, RMS norm, Muon
 class _Launch:
     """The stream one call is enqueued on.  Every tensor must be contiguous and on one CUDA
     device; while the object is entered, that device and the call's stream are current, so that
@@ -707,3 +712,42 @@ def dp_rmsnorm_step(H, gain, dY, C, sigma, seed, step, layer_id, eps=1e-6, resid
                     _ptr(norms_out), _ptr(G_out), _ptr(ws), _ws_bytes(ws), s),
               "dp_rmsnorm_step")
     return dX, G_out, norms_out
+
+
+def muon_workspace_size(rows, cols):
+    return int(lib().dp_muon_workspace_size(rows, cols))
+
+
+def dp_orthogonalize(G, steps=5, U=None, workspace=None, stream=None):
+    """G [rows, cols] (fp32 or bf16) orthogonalised by `steps` Newton-Schulz products, in bf16."""
+    import torch
+
+    if G.dim() != 2:
+        raise ValueError("G must be [rows, cols]")
+    rows, cols = int(G.shape[0]), int(G.shape[1])
+    _expect(U, "U", (rows, cols), torch.bfloat16)
+    with _Launch(stream, G=G, U=U, workspace=workspace) as s:
+        ws = _scratch(workspace, muon_workspace_size(rows, cols), G.device, "dp_muon_workspace_size")
+        U = torch.empty(rows, cols, dtype=torch.bfloat16, device=G.device) if U is None else U
+        check(lib().dp_orthogonalize(_ptr(G), _dtype_code(G), rows, cols, int(steps), _ptr(U), _ptr(ws),
+                                     _ws_bytes(ws), s), "dp_orthogonalize")
+    return U
+
+
+def dp_muon_step(W, R, M, lr, momentum=0.95, nesterov=True, weight_decay=0.0, grad_scale=1.0, update_scale=1.0,
+                 steps=5, workspace=None, stream=None):
+    """One Muon update of W [d_in, d_out] with the privatised gradient R and the momentum M, both
+    W and M in place (fp32); returns (W, M)."""
+    import torch
+
+    if W.dim() != 2:
+        raise ValueError("W must be [d_in, d_out]")
+    for name, t in (("W", W), ("R", R), ("M", M)):
+        _expect(t, name, W.shape, torch.float32)
+    d_in, d_out = int(W.shape[0]), int(W.shape[1])
+    with _Launch(stream, W=W, R=R, M=M, workspace=workspace) as s:
+        ws = _scratch(workspace, muon_workspace_size(d_in, d_out), W.device, "dp_muon_workspace_size")
+        check(lib().dp_muon_step(_ptr(W), _ptr(R), _ptr(M), d_in, d_out, float(lr), float(momentum),
+                                 1 if nesterov else 0, float(weight_decay), float(grad_scale), float(update_scale),
+                                 int(steps), _ptr(ws), _ws_bytes(ws), s), "dp_muon_step")
+    return W, M

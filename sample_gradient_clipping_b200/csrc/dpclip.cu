@@ -19,6 +19,7 @@
 #include "dpclip.h"
 #include "embedding.cuh"
 #include "launch_profiler.h"
+#include "muon.cuh"
 #include "nvtx_range.h"
 #include "rmsnorm.cuh"
 #include "rng.cuh"
@@ -2381,3 +2382,4 @@ long long dp_kernel_launches(void) { return profiler().launches.load(); }
 
 #include "embedding_host.cuh"
 #include "rmsnorm_host.cuh"
+#include "muon_host.cuh"

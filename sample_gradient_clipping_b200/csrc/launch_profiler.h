@@ -39,6 +39,9 @@ enum KernelKind : int {
   kKindRmsNorm,       // RMS norm with the residual's addition
   kKindRmsNormBackward,  // its backward, with the gain gradient's partial sums
   kKindRmsNormGain,   // the gain's per-sample gradients and their clipped sum + noise
+  kKindMuonMomentum,  // momentum and its norm
+  kKindMuonPrepare,   // the fp16 planes of the normalised momentum
+  kKindNsProduct,     // tcgen05 products of the Newton-Schulz steps
   kNumKinds
 };
 
@@ -48,7 +51,7 @@ inline const char* kernel_kind_name(int k) {
       "f32_norm",   "f32_clipsum",  "f32_project",   "umma_clipsum",    "umma_explicit_norm",
       "umma_ghost_norm", "umma_project", "umma_explicit_store", "clip_reduce", "adam_rspace",
       "umma_axpy", "umma_ghost_shared", "split_combine", "embedding_lookup", "embedding_sort", "embedding_norm",
-      "embedding_sum", "rmsnorm", "rmsnorm_backward", "rmsnorm_gain"};
+      "embedding_sum", "rmsnorm", "rmsnorm_backward", "rmsnorm_gain", "muon_momentum", "muon_prepare", "ns_product"};
   return (k >= 0 && k < kNumKinds) ? names[k] : "";
 }
 

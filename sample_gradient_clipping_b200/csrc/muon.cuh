@@ -1,0 +1,592 @@
+// The Muon step: momentum, orthogonalisation of the momentum by Newton-Schulz products, update.
+//
+//   M <- mu M + g, g = grad_scale R;  U0 = g + mu M (Nesterov) or M;  X = U0 / (||U0||_F + 1e-7);
+//   steps times:  A = X X^T,  X <- a X + (b A + c A^2) X,  (a, b, c) = (3.4445, -4.7750, 2.0315);
+//   W <- (1 - lr weight_decay) W - lr update_scale X.
+// Every singular value of X goes through x <- a x + b x^3 + c x^5, which drives it towards 1; the
+// singular vectors stay.  X is kept as [m, n] with m <= n (a tall matrix transposed), so that A is
+// the smaller Gram matrix.
+//
+// The products run on the tensor cores in fp16 with fp32 accumulation: all values are at most
+// about 1 here, so fp16's 11 bits serve where bf16 would keep 8.  Three choices keep five steps on a
+// noisy gradient within 1e-3 of the exact iteration (3e-3 without them, 1.5e-2 with bf16 operands):
+//   - X is held as two fp16 planes, hi + lo 2^-11.  Products read hi; the term a X, by which small
+//     singular values grow 3.4 times a step, uses both, so their rounding does not grow with them.
+//   - b A and c A^2 use the same rounded A, so the polynomial is exact in the matrix that is stored.
+//   - B = b A + c A^2 is stored less delta I, and a + delta multiplies X instead.  Near convergence
+//     B is about -2.7 I; with delta the polynomial at the mean eigenvalue tr(A) / m, the large
+//     diagonal stays in fp32 and only the small rest is rounded.
+//
+// The three products of a step are three launches of one engine (ns_kernel): the tcgen05 pipeline
+// of umma_gemm_2sm.cuh with 256 x 256 tiles on SM pairs, or 128 x 128 tiles on single SMs where
+// those would leave most SMs idle.  A and B are symmetric: only tiles on and above the diagonal
+// are formed, and each is stored a second time transposed.
+#pragma once
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "embedding.cuh"
+#include "ptx.cuh"
+#include "simt.cuh"
+#include "umma_gemm_2sm.cuh"
+
+namespace dpclip {
+
+constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+constexpr double kNsEps = 1e-7;
+constexpr float kLoScale = 2048.0f;  // the lo plane holds (x - hi) 2^11, a normal fp16 wherever hi is
+
+enum NsKind : int { kNsGram = 0, kNsPoly = 1, kNsApply = 2 };
+// Where kNsApply's result goes: the next step's planes; U in bf16, or W, as they lie or transposed.
+enum NsOut : int { kNsPlanes = 0, kNsU = 1, kNsUT = 2, kNsW = 3, kNsWT = 4 };
+
+struct alignas(64) NsParams {
+  CUtensorMap tmA, tmB;
+  int m, n;               // rows and columns of the result (kNsGram, kNsPoly: m x m)
+  int tiles_m, tiles_n;   // tiles of the result; symmetric kinds: tiles_m on a side
+  int num_units, k_blocks;
+  const __half* A;        // kNsPoly: A
+  const __half *hi, *lo;  // kNsApply: X
+  __half *out, *out_lo;   // A or B; the next X's planes
+  float* trace;           // one partial per 32 rows of A
+  int order;              // rows of A (m of the iteration)
+  int out_mode;           // NsOut
+  __nv_bfloat16* U;
+  float* W;
+  float keep, rate;       // W <- keep W - rate X
+  uint32_t* status;
+};
+
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4)                                 // D: f32; A and B format 0: f16
+         | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <bool PAIR_, int KIND_>
+struct NsConfig {
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int KIND = KIND_;
+  static constexpr int BM = 128;                       // rows a CTA
+  static constexpr int TILE = PAIR ? 256 : 128;        // the tile is square
+  static constexpr int BK = 64;
+  static constexpr bool SYMMETRIC = KIND != kNsApply;
+  static constexpr bool B_MN = KIND == kNsApply;       // X as [k, n]: its columns are contiguous
+  static constexpr int OP_BYTES = BM * BK * 2;         // 16 KB of each operand a CTA and stage
+  static constexpr int STAGE_BYTES = 2 * OP_BYTES;
+  static constexpr int STAGES = 6;
+  static constexpr int NUM_BUFS = 2;
+  static constexpr int THREADS = 192;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;
+  static constexpr uint32_t IDESC = umma_idesc_f16(PAIR ? 256 : 128, TILE, false, B_MN);
+  static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per block");
+};
+
+struct NsUnit {
+  int mb, nb;  // tile row and column
+};
+
+template <class Cfg>
+__device__ __forceinline__ NsUnit ns_unit(const NsParams& p, int u) {
+  NsUnit w;
+  if constexpr (Cfg::SYMMETRIC) {  // pairs mb <= nb, row by row
+    int row = 0;
+    while (u >= p.tiles_m - row) {
+      u -= p.tiles_m - row;
+      ++row;
+    }
+    w.mb = row;
+    w.nb = row + u;
+  } else {  // groups of 8 row tiles, so that CTAs running together share operand tiles in L2
+    constexpr int G = 8;
+    const int per = G * p.tiles_n;
+    const int first = (u / per) * G;
+    const int rows = min(G, p.tiles_m - first);
+    w.mb = first + (u % per) % rows;
+    w.nb = (u % per) / rows;
+  }
+  return w;
+}
+
+// delta = b t + c t^2 at t = tr(A) / order, by every warp in the same order.
+__device__ __forceinline__ float ns_delta(const float* __restrict__ trace, int order, uint32_t lane) {
+  float t = 0.0f;
+  for (int k = static_cast<int>(lane); k < (order + 31) / 32; k += 32) t += __ldcg(trace + k);
+  t = warp_sum(t) / static_cast<float>(order);
+  return t * fmaf(kNsC, t, kNsB);
+}
+
+// The 128 rows of a unit that this CTA holds: row0 + 32 wq + lane is this thread's.
+template <class Cfg>
+__device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsUnit& w, int row0, uint32_t tacc, int wq,
+                                            uint32_t lane, float delta) {
+  const int r = row0 + wq * 32 + static_cast<int>(lane);
+  const bool row_ok = r < p.m;
+  float tr = 0.0f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < Cfg::TILE; c0 += 32) {
+    float v[32];
+    __syncwarp();
+    tmem_ld32(tacc + c0, v);
+    tmem_ld_wait();
+    const int col = w.nb * Cfg::TILE + c0;
+    const int cols = min(32, p.n - col);  // a multiple of 8
+    if (cols <= 0) continue;              // the same for the whole warp
+    if constexpr (Cfg::KIND == kNsApply) {
+      if (row_ok) {
+        const long long at = static_cast<long long>(r) * p.n + col;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (8 * q >= cols) break;
+          const uint4 h4 = *reinterpret_cast<const uint4*>(p.hi + at + 8 * q);
+          const uint4 l4 = *reinterpret_cast<const uint4*>(p.lo + at + 8 * q);
+          const __half2* h = reinterpret_cast<const __half2*>(&h4);
+          const __half2* l = reinterpret_cast<const __half2*>(&l4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = __half22float2(h[e]), b = __half22float2(l[e]);
+            v[8 * q + 2 * e] = fmaf(kNsA + delta, fmaf(b.x, 1.0f / kLoScale, a.x), v[8 * q + 2 * e]);
+            v[8 * q + 2 * e + 1] = fmaf(kNsA + delta, fmaf(b.y, 1.0f / kLoScale, a.y), v[8 * q + 2 * e + 1]);
+          }
+        }
+      }
+    } else if constexpr (Cfg::KIND == kNsPoly) {
+      if (row_ok) {
+        const long long at = static_cast<long long>(r) * p.n + col;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (8 * q >= cols) break;
+          const uint4 a4 = *reinterpret_cast<const uint4*>(p.A + at + 8 * q);
+          const __half2* h = reinterpret_cast<const __half2*>(&a4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = __half22float2(h[e]);
+            v[8 * q + 2 * e] = fmaf(kNsB, a.x, kNsC * v[8 * q + 2 * e]);
+            v[8 * q + 2 * e + 1] = fmaf(kNsB, a.y, kNsC * v[8 * q + 2 * e + 1]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (col + e == r) v[e] -= delta;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (col + e == r) tr = v[e];
+    }
+
+    const int mode = Cfg::KIND == kNsApply ? p.out_mode : kNsPlanes;
+    if (mode == kNsPlanes) {
+      if (row_ok) {
+        const long long at = static_cast<long long>(r) * p.n + col;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (8 * q >= cols || !DP_DCHECK(at + 8 * q + 8 <= static_cast<long long>(p.m) * p.n, 60u, p.status)) break;
+          uint4 h4, l4;
+          __half2* h = reinterpret_cast<__half2*>(&h4);
+          __half2* l = reinterpret_cast<__half2*>(&l4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[e] = __floats2half2_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+            if constexpr (Cfg::KIND == kNsApply) {
+              const float2 a = __half22float2(h[e]);
+              l[e] = __floats2half2_rn((v[8 * q + 2 * e] - a.x) * kLoScale, (v[8 * q + 2 * e + 1] - a.y) * kLoScale);
+            }
+          }
+          *reinterpret_cast<uint4*>(p.out + at + 8 * q) = h4;
+          if constexpr (Cfg::KIND == kNsApply) *reinterpret_cast<uint4*>(p.out_lo + at + 8 * q) = l4;
+        }
+        if constexpr (Cfg::SYMMETRIC) {  // the tile below the diagonal: column e of this one is its row
+          if (w.mb != w.nb) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e < cols) p.out[static_cast<long long>(col + e) * p.m + r] = __float2half_rn(v[e]);
+          }
+        }
+      }
+    } else if (mode == kNsU) {
+      if (row_ok) {
+        __nv_bfloat16* dst = p.U + static_cast<long long>(r) * p.n + col;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (8 * q >= cols) break;
+          uint4 pk;
+          __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&pk);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+          *reinterpret_cast<uint4*>(dst + 8 * q) = pk;
+        }
+      }
+    } else if (mode == kNsUT) {
+      if (row_ok) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e < cols) p.U[static_cast<long long>(col + e) * p.m + r] = __float2bfloat16_rn(v[e]);
+      }
+    } else if (mode == kNsW) {
+      if (row_ok) {
+        float4* dst = reinterpret_cast<float4*>(p.W + static_cast<long long>(r) * p.n + col);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (4 * q >= cols) break;
+          float4 o = dst[q];
+          o.x = fmaf(p.keep, o.x, -p.rate * v[4 * q]);
+          o.y = fmaf(p.keep, o.y, -p.rate * v[4 * q + 1]);
+          o.z = fmaf(p.keep, o.z, -p.rate * v[4 * q + 2]);
+          o.w = fmaf(p.keep, o.w, -p.rate * v[4 * q + 3]);
+          dst[q] = o;
+        }
+      }
+    } else {
+      if (row_ok) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (e < cols) {
+            float* dst = p.W + static_cast<long long>(col + e) * p.m + r;
+            *dst = fmaf(p.keep, *dst, -p.rate * v[e]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (Cfg::KIND == kNsGram) {
+    if (w.mb == w.nb) {  // rows past m were zero-filled and add nothing
+      tr = warp_sum(tr);
+      if (lane == 0 && row0 + wq * 32 < p.m) p.trace[(row0 + wq * 32) / 32] = tr;
+    }
+  }
+}
+
+template <class Cfg>
+__device__ __forceinline__ void ns_body(const NsParams& p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::STAGES * Cfg::STAGE_BYTES);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + Cfg::STAGES;
+  uint64_t* acc_full = bars + 2 * Cfg::STAGES;
+  uint64_t* acc_empty = acc_full + Cfg::NUM_BUFS;
+  uint64_t* drain = acc_empty + Cfg::NUM_BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  constexpr bool PAIR = Cfg::PAIR;
+  constexpr int kCtas = PAIR ? 2 : 1;
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const bool leader = rank == 0;
+  const int first = blockIdx.x / kCtas;
+  const int step = gridDim.x / kCtas;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(smem_addr(full + s), 1);
+      mbar_init(smem_addr(empty + s), 1);
+    }
+    for (int b = 0; b < Cfg::NUM_BUFS; ++b) {
+      mbar_init(smem_addr(acc_full + b), 1);
+      mbar_init(smem_addr(acc_empty + b), 4 * kCtas);  // one arrival per epilogue warp of the tile
+    }
+    mbar_init(smem_addr(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_addr(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_addr(tmem_slot), 512);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();  // barriers and TMEM are ready; global memory only from here
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (every CTA)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = first; ok && u < p.num_units; u += step) {
+        const NsUnit w = ns_unit<Cfg>(p, u);
+        const int a0 = w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
+        const int b0 = w.nb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;  // its half of B (PAIR), all of it else
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait_bounded(smem_addr(empty + stage), phase ^ 1u, abort_flag, p.status, 21u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sA = smem_addr(smem + stage * Cfg::STAGE_BYTES);
+          const uint32_t sB = sA + Cfg::OP_BYTES;
+          const int k0 = kb * Cfg::BK;
+          if (leader) mbar_arrive_expect_tx(smem_addr(full + stage), kCtas * Cfg::STAGE_BYTES);
+          if constexpr (PAIR) {
+            const uint32_t bar = map_to_rank(smem_addr(full + stage), 0);
+            tma_load_2d_pair(sA, &p.tmA, bar, k0, a0);
+            if constexpr (Cfg::B_MN) {
+              tma_load_2d_pair(sB, &p.tmB, bar, b0, k0);
+              tma_load_2d_pair(sB + Cfg::BK * 128, &p.tmB, bar, b0 + 64, k0);
+            } else {
+              tma_load_2d_pair(sB, &p.tmB, bar, k0, b0);
+            }
+          } else {
+            const uint32_t bar = smem_addr(full + stage);
+            tma_load_2d(sA, &p.tmA, bar, k0, a0);
+            if constexpr (Cfg::B_MN) {
+              tma_load_2d(sB, &p.tmB, bar, b0, k0);
+              tma_load_2d(sB + Cfg::BK * 128, &p.tmB, bar, b0 + 64, k0);
+            } else {
+              tma_load_2d(sB, &p.tmB, bar, k0, b0);
+            }
+          }
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int buf = 0;
+      uint32_t buf_phase = 0;
+      bool ok = true;
+      for (int u = first; ok && u < p.num_units; u += step) {
+        if (!mbar_wait_bounded(smem_addr(acc_empty + buf), buf_phase ^ 1u, abort_flag, p.status, 22u)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * 256;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait_bounded(smem_addr(full + stage), phase, abort_flag, p.status, 23u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sA = smem_addr(smem + stage * Cfg::STAGE_BYTES);
+          const uint32_t sB = sA + Cfg::OP_BYTES;
+#pragma unroll
+          for (int ks = 0; ks < Cfg::BK / 16; ++ks) {
+            const uint64_t da = umma_desc_sw128(sA + ks * 32, 16, 1024);
+            const uint64_t db = Cfg::B_MN ? umma_desc_sw128(sB + ks * 2048, Cfg::BK * 128, 1024)
+                                          : umma_desc_sw128(sB + ks * 32, 16, 1024);
+            // (These issue tcgen05.mma kind::f16; the instruction descriptor says fp16 operands.)
+            if constexpr (PAIR)
+              umma_bf16_pair(d_tmem, da, db, Cfg::IDESC, (kb > 0 || ks > 0) ? 1u : 0u);
+            else
+              umma_bf16(d_tmem, da, db, Cfg::IDESC, (kb > 0 || ks > 0) ? 1u : 0u);
+          }
+          if constexpr (PAIR)
+            umma_commit_pair(smem_addr(empty + stage), 0x3);
+          else
+            umma_commit(smem_addr(empty + stage));
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if constexpr (PAIR)
+          umma_commit_pair(smem_addr(acc_full + buf), 0x3);
+        else
+          umma_commit(smem_addr(acc_full + buf));
+        if (++buf == Cfg::NUM_BUFS) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      // No MMA may still write TMEM when it is released.
+      if constexpr (PAIR)
+        umma_commit_pair_local(smem_addr(drain));
+      else
+        umma_commit(smem_addr(drain));
+      const unsigned long long t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_addr(drain), 0u)) {
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+          if (p.status) atomicCAS(p.status, 0u, 25u);
+          break;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue warps 2..5 (every CTA)
+    const int wq = warp & 3;
+    const float delta = Cfg::KIND == kNsGram ? 0.0f : ns_delta(p.trace, p.order, lane);
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    for (int u = first; u < p.num_units; u += step) {
+      const NsUnit w = ns_unit<Cfg>(p, u);
+      if (!mbar_wait_bounded(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 24u)) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + buf * 256 + (static_cast<uint32_t>(wq * 32) << 16);
+      ns_epilogue<Cfg>(p, w, w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM, tacc, wq, lane, delta);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_remote(map_to_rank(smem_addr(acc_empty + buf), 0));
+        else
+          mbar_arrive(smem_addr(acc_empty + buf));
+      }
+      if (++buf == Cfg::NUM_BUFS) {
+        buf = 0;
+        buf_phase ^= 1u;
+      }
+    }
+  }
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // no CTA leaves while its peer may still signal it
+  griddep_launch_dependents();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1) ns_kernel(const __grid_constant__ NsParams p) {
+  ns_body<Cfg>(p);
+}
+template <class Cfg>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+    ns_pair_kernel(const __grid_constant__ NsParams p) {
+  ns_body<Cfg>(p);
+}
+
+// ------------------------------------------------------------------------------ around them
+constexpr int kMuonThreads = 256;
+
+// MUON: M <- mu M + gs R, and u = gs R + mu M (nesterov) or M; else u = R.  Block partials of
+// sum u^2, in fp64 (the squares of large or tiny gradients leave fp32's range).
+template <typename T, bool MUON>
+__global__ void __launch_bounds__(kMuonThreads)
+    muon_momentum_kernel(const T* __restrict__ R, float* __restrict__ M, long long vecs, float mu, float gs,
+                         int nesterov, double* __restrict__ partials, uint32_t* __restrict__ status) {
+  griddep_enter();
+  constexpr int V = EmbVec<T>::N;
+  __shared__ double part[kMuonThreads / 32];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+  const long long stride = static_cast<long long>(gridDim.x) * kMuonThreads;
+  double ss = 0.0;
+  constexpr int kU = 4;
+  for (long long v0 = static_cast<long long>(blockIdx.x) * kMuonThreads + threadIdx.x; v0 < vecs; v0 += kU * stride) {
+    uint4 q[kU], qm[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (v0 + k * stride >= vecs) continue;
+      q[k] = __ldg(reinterpret_cast<const uint4*>(R) + v0 + k * stride);
+      if constexpr (MUON) qm[k] = reinterpret_cast<const uint4*>(M)[v0 + k * stride];
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (v0 + k * stride >= vecs) continue;
+      float u[V];
+      unpack16(q[k], u, R);
+      if constexpr (MUON) {
+        float m[4];
+        unpack16(qm[k], m, M);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float g = gs * u[e];
+          m[e] = fmaf(mu, m[e], g);
+          u[e] = nesterov ? fmaf(mu, m[e], g) : m[e];
+        }
+        reinterpret_cast<uint4*>(M)[v0 + k * stride] =
+            make_uint4(__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3]));
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) ss = fma(static_cast<double>(u[e]), static_cast<double>(u[e]), ss);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = ss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int w = 0; w < kMuonThreads / 32; ++w) s += part[w];
+    partials[blockIdx.x] = s;
+  }
+}
+
+// 1 / (sqrt(sum of the partials) + eps), by every block in the same order.
+__device__ __forceinline__ double muon_inverse_norm(const double* __restrict__ partials, int count) {
+  __shared__ double part[kMuonThreads / 32];
+  double s = 0.0;
+  for (int k = threadIdx.x; k < count; k += kMuonThreads) s += partials[k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int w = 0; w < kMuonThreads / 32; ++w) s += part[w];
+  return 1.0 / (sqrt(s) + kNsEps);
+}
+
+// The planes of X = u / (||u|| + eps): 64 x 64 tiles through shared memory when the matrix is tall
+// (TRANSPOSE: X[c, r] = u[r, c]), straight through registers otherwise.
+template <typename T, bool MUON, bool TRANSPOSE>
+__global__ void __launch_bounds__(kMuonThreads)
+    muon_prepare_kernel(const T* __restrict__ R, const float* __restrict__ M, int rows, int cols, float mu, float gs,
+                        int nesterov, const double* __restrict__ partials, int count, __half* __restrict__ hi,
+                        __half* __restrict__ lo) {
+  griddep_enter();
+  const double inv = muon_inverse_norm(partials, count);
+  auto value = [&](long long at) {
+    float u;
+    if constexpr (MUON) {
+      const float m = M[at];
+      u = nesterov ? fmaf(mu, m, gs * static_cast<float>(R[at])) : m;
+    } else {
+      u = static_cast<float>(R[at]);
+    }
+    return static_cast<float>(static_cast<double>(u) * inv);
+  };
+  auto put = [&](long long at, float a, float b) {  // two neighbours
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    *reinterpret_cast<__half2*>(hi + at) = h;
+    *reinterpret_cast<__half2*>(lo + at) = __floats2half2_rn((a - f.x) * kLoScale, (b - f.y) * kLoScale);
+  };
+  if constexpr (TRANSPOSE) {
+    __shared__ float tile[64][65];
+    const int tc = (cols + 63) / 64;
+    const long long tiles = static_cast<long long>((rows + 63) / 64) * tc;
+    for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int r0 = static_cast<int>(t / tc) * 64, c0 = static_cast<int>(t % tc) * 64;
+      for (int k = threadIdx.x; k < 64 * 64; k += kMuonThreads) {
+        const int r = r0 + k / 64, c = c0 + k % 64;
+        tile[k / 64][k % 64] = r < rows && c < cols ? value(static_cast<long long>(r) * cols + c) : 0.0f;
+      }
+      __syncthreads();
+      for (int k = threadIdx.x; k < 64 * 32; k += kMuonThreads) {
+        const int c = c0 + k / 32, r = r0 + 2 * (k % 32);  // rows come in multiples of 8
+        if (c < cols && r < rows)
+          put(static_cast<long long>(c) * rows + r, tile[2 * (k % 32)][k / 32], tile[2 * (k % 32) + 1][k / 32]);
+      }
+      __syncthreads();
+    }
+  } else {
+    const long long pairs = static_cast<long long>(rows) * cols / 2;
+    const long long stride = static_cast<long long>(gridDim.x) * kMuonThreads;
+#pragma unroll 4
+    for (long long k = static_cast<long long>(blockIdx.x) * kMuonThreads + threadIdx.x; k < pairs; k += stride)
+      put(2 * k, value(2 * k), value(2 * k + 1));
+  }
+}
+
+}  // namespace dpclip

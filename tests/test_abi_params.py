@@ -135,3 +135,34 @@ def test_rmsnorm_workspace_size(L):
     parts = 8 * 74 * 4096 * 4
     assert parts + 8 * 4096 * 4 <= f(8, 2048, 4096, BF16) < parts + 8 * 4096 * 4 + 4096
     assert f(8, 2048, 12, BF16) == 0 and f(8, 2048, 16392, BF16) == 0 and f(1, 1, 4, F32) > 0
+
+
+def test_muon_rejects_on_host(L):
+    def ortho(**k):
+        a = dict(dict(G=FAKE, dt=F32, m=64, n=32, steps=5, U=FAKE + 64, ws=FAKE, n_ws=1 << 30), **k)
+        return L.dp_orthogonalize(a["G"], a["dt"], a["m"], a["n"], a["steps"], a["U"], a["ws"], a["n_ws"], None)
+
+    for k in (dict(G=None), dict(G=ODD), dict(dt=3), dict(m=0), dict(m=12), dict(n=4), dict(n=36), dict(steps=0),
+              dict(steps=33), dict(U=None), dict(U=ODD), dict(U=FAKE), dict(ws=None), dict(ws=FAKE + 16),
+              dict(m=131072, n=131080), dict(m=65544, n=65544)):
+        assert ortho(**k) == E, k
+    assert ortho(n_ws=1000) == W
+
+    def muon(**k):
+        a = dict(dict(W=FAKE, R=FAKE + 64, M=FAKE + 128, m=64, n=32, lr=0.1, mu=0.9, wd=0.0, gs=1.0, us=1.0, steps=5,
+                      ws=FAKE, n_ws=1 << 30), **k)
+        return L.dp_muon_step(a["W"], a["R"], a["M"], a["m"], a["n"], a["lr"], a["mu"], 1, a["wd"], a["gs"], a["us"],
+                              a["steps"], a["ws"], a["n_ws"], None)
+
+    for k in (dict(W=None), dict(W=ODD), dict(R=None), dict(R=ODD), dict(R=FAKE), dict(M=None), dict(M=ODD), dict(M=FAKE),
+              dict(M=FAKE + 64), dict(m=12), dict(lr=-1.0), dict(lr=math.inf), dict(lr=math.nan), dict(mu=1.0),
+              dict(mu=-0.1), dict(mu=math.nan), dict(wd=-1.0), dict(wd=math.inf), dict(gs=math.nan), dict(us=math.inf),
+              dict(steps=0), dict(steps=33), dict(ws=None), dict(ws=FAKE + 16)):
+        assert muon(**k) == E, k
+    assert muon(n_ws=1000) == W
+
+
+def test_muon_workspace_size(L):
+    f = L.dp_muon_workspace_size
+    assert 8 * 64 * 32 + 4 * 32 * 32 <= f(64, 32) < 8 * 64 * 32 + 4 * 32 * 32 + 16384
+    assert f(64, 32) == f(32, 64) and f(64, 12) == 0 and f(0, 8) == 0
