@@ -326,7 +326,7 @@ dp_status dp_embedding_lookup(const void* W, dp_dtype w_dt, const void* ids, dp_
                               long long N, int V, int d, void* Y, dp_dtype y_dt, void* stream);
 
 /* Workspace bytes of the three calls below (0 when the shape is invalid): about
- * 4 B*T (6 + d/256) + B*T d/4 + 8 V bytes. */
+ * B*T (18 + d/4) + 8 V bytes. */
 size_t dp_embedding_workspace_size(int B, int T, int V, int d, dp_dtype dt);
 
 /* norms[i] = ||G_i||, as dp_per_sample_norms. */

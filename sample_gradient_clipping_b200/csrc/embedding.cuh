@@ -6,12 +6,13 @@
 //   S[v]  = scale sum_i c_i (sum of group (i, v)) + sigma C z.
 // As a linear layer it would be a one-hot X of V columns; here the tokens are sorted instead:
 //   emb_sort_kernel  a stable radix sort of the tokens by id.  Token n = i T + t, so each id's run
-//                    is ordered by sample and each group is contiguous; the kernel also lists the
-//                    groups and the rows that occur.
-//   emb_norm_kernel  the sum of every group, squared, into a slot of the group's first token; the
-//                    sum of a long group is kept in fp32, since the last kernel needs it again.
-//   emb_norms_kernel n_i from the sample's slots, in a fixed order in fp64.
-//   emb_sum_kernel   every row of S: its groups times their clip factors, plus the noise.
+//                    is ordered by sample, and each group is contiguous;
+//   emb_mark_kernel  finds the groups and rows in that order (a small sort does so itself);
+//   emb_norm_kernel  puts the square of each group's sum into the slot of its first token; the sum
+//                    of a long group is kept in fp32, since the last kernel needs it again;
+//   emb_norms_kernel n_i from the sample's slots, in a fixed order in fp64;
+//   emb_sum_kernel   every row of S: its tokens' rows (or its long groups' sums) times their clip
+//                    factors, plus the noise.
 // dY is read twice (the norm decides the factor of every row before any row can be added), S is
 // written once.  Nothing is added with floating-point atomics, so the bits repeat.
 // A token whose id is negative, at or past V, or the padding index belongs to no group; an id at
@@ -31,8 +32,8 @@ namespace dpclip {
 // Status word of an id at or past V (a timeout's site is below it, a debug check's above).
 constexpr uint32_t kStatusIdRange = 900u;
 
-constexpr int kEmbSortCtas = 8;       // one cluster: its barriers are the passes' barriers
 constexpr int kEmbSortThreads = 1024;
+constexpr int kEmbSortWarps = kEmbSortThreads / 32;
 constexpr int kEmbRadix = 256;
 // A group of more tokens than this is summed by a whole block, and its sum kept: the last kernel
 // then reads 4 bytes an element once instead of its rows (2 bytes each in bf16).
@@ -42,21 +43,28 @@ constexpr int kEmbHeavyRow = 64;
 constexpr int kEmbThreads = 256;
 constexpr int kEmbWarps = kEmbThreads / 32;
 
-enum EmbCount : int { kEmbGroups = 0, kEmbLong = 1, kEmbHeavy = 2 };
+// What the last kernel does at a sorted position: add the token's row; nothing, inside a long
+// group; add the long group's sum, at its first position.
+enum EmbUse : uint8_t { kEmbRow = 0, kEmbSkip = 1, kEmbLongSum = 2, kEmbUseMask = 3 };
+constexpr uint8_t kEmbHead = 4;  // beside it: a group starts here (or the tokens without one do)
 
-// The sorted tokens of one call (all device pointers into the workspace).
+// The slot of a long group's sum: two groups of more than kEmbLongGroup tokens start at least
+// that many + 1 positions apart.
+__host__ __device__ constexpr long long emb_slot(long long first) { return first / (kEmbLongGroup + 1); }
+
+// The sorted tokens of one call (device pointers into the workspace).
 struct EmbIndex {
-  uint32_t* keys[2];     // [N] ids, ping-pong between the passes
-  uint32_t* toks[2];     // [N] tokens
-  int last;              // which of the two holds the sorted order
-  uint32_t* counts;      // EmbCount
-  uint32_t* row_first;   // [V] 1 + first group of the row, 0: the row does not occur
-  uint32_t* row_end;     // [V] one past its last group (rows that occur)
-  uint32_t* group_pos;   // [groups + 1] first sorted position of the group
-  int* group_long;       // [groups] slot of a long group's sum, or -1
-  uint32_t* long_list;   // groups by slot
-  uint32_t* heavy_list;  // rows
-  float* sq;             // [N][chunks] squared sums, by first token of the group
+  const uint32_t* keys;  // [N] ids in order, V for a token without a group
+  const uint32_t* toks;  // [N] their tokens
+  uint32_t* heavies;     // how many heavy rows are listed
+  uint32_t* heavy_list;  // their ids
+  uint32_t* longs;       // how many long groups are listed
+  uint2* long_list;      // their (first, end) positions
+  uint2* rows;           // [V] (1 + first position, end position); (0, -): the row does not occur
+  uint8_t* use;          // [N] EmbUse | kEmbHead
+  uint32_t* turns;       // [chunks of emb_sum_kernel] rows handed out
+  float* sq;             // [N][chunks] squared sums, by first token of the group; 0 elsewhere
+  int chunks;            // of emb_norm_kernel
   float* long_sums;      // [slots][d]
 };
 
@@ -160,12 +168,6 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t local, uint32_t rank
   return v;
 }
 
-// The cluster's barrier, after the threads of each warp have met again.
-__device__ __forceinline__ void emb_cluster_sync() {
-  __syncwarp();
-  cluster_sync_all();
-}
-
 // The id of token n as a sort key: V for a token that belongs to no group.
 __device__ __forceinline__ uint32_t emb_key(const void* ids, int index64, long long n, int V, long long padding,
                                             uint32_t* status) {
@@ -174,85 +176,213 @@ __device__ __forceinline__ uint32_t emb_key(const void* ids, int index64, long l
   return (id < 0 || id >= V || id == padding) ? static_cast<uint32_t>(V) : static_cast<uint32_t>(id);
 }
 
-// Sorts the N tokens by key in `passes` stable passes of 8 bits, then lists the groups.  One
-// cluster of 8 blocks: token ranges are contiguous per block and per warp, so a warp's rank within
-// a digit is (digits below) + (blocks before) + (warps before) + (its own so far), and the only
-// exchange is each block's 256 digit totals through distributed shared memory.  All the work is
-// latency (a few microseconds a pass at 16384 tokens), which one launch keeps smallest.
-__global__ void __cluster_dims__(kEmbSortCtas, 1, 1) __launch_bounds__(kEmbSortThreads, 1)
-    emb_sort_kernel(const void* __restrict__ ids, int index64, long long N, int T, int V, long long padding,
-                    int passes, EmbIndex ix, long long sq_len, uint32_t* __restrict__ status) {
+// The end of the group of (key, sample) that starts at sorted position `first`, at most T positions
+// on: a 32-way search by one warp.
+__device__ __forceinline__ uint32_t emb_group_end(const EmbIndex& ix, uint32_t key, uint32_t sample, long long first,
+                                                  long long N, uint32_t T, uint32_t lane) {
+  long long lo = first, hi = first + T < N ? first + T : N;  // lo is inside, hi is not
+  while (hi - lo > 1) {
+    const long long step = (hi - lo + 31) / 32;
+    const long long at = lo + step * (lane + 1);
+    const bool inside = at < hi && __ldcg(ix.keys + at) == key && __ldcg(ix.toks + at) / T == sample;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, inside));
+    const long long next = lo + step * (n + 1);
+    hi = next < hi ? next : hi;
+    lo += step * n;
+  }
+  return static_cast<uint32_t>(hi);
+}
+
+// Marks 32 sorted positions from p0: which start a group or a row, which lie in a long group, what
+// the norm kernel's slots start from.  A long group is seen from the heads of three windows of 32:
+// if none lies within 32 positions on one side, the group is long.  One warp.
+__device__ __forceinline__ void emb_mark(const EmbIndex& ix, long long p0, long long N, uint32_t T, uint32_t none,
+                                         uint32_t lane) {
+  // The heads of a window, and this lane's key and token in the middle one.
+  uint32_t my_key = none, my_tok = 0;
+  bool my_row_head = false;
+  auto heads = [&](long long w0, bool mine) {
+    const long long p = w0 + lane;
+    bool head = p >= N;  // the end closes the last group
+    if (p >= 0 && p < N) {
+      const uint32_t key = __ldcg(ix.keys + p), tok = __ldcg(ix.toks + p);
+      const uint32_t last_key = p > 0 ? __ldcg(ix.keys + p - 1) : none + 1u, last_tok = p > 0 ? __ldcg(ix.toks + p - 1) : 0u;
+      const bool row_head = key != last_key;
+      head = row_head || (key != none && tok / T != last_tok / T);
+      if (mine) {
+        my_key = key;
+        my_tok = tok;
+        my_row_head = row_head;
+      }
+    }
+    return __ballot_sync(0xFFFFFFFFu, head);
+  };
+  const uint32_t before = heads(p0 - 32, false), here = heads(p0, true), after = heads(p0 + 32, false);
+  const uint32_t row_heads = __ballot_sync(0xFFFFFFFFu, my_row_head || p0 + lane >= N);
+  const long long p = p0 + lane;
+  const uint32_t upto = 0xFFFFFFFFu >> (31u - lane), past = ~upto;
+  // First and end position of the group, relative to p0; "far" where no head is in sight.
+  const bool head = (here >> lane) & 1u;
+  const int first = (here & upto) ? 31 - __clz(here & upto) : before ? -1 - __clz(before) : -1000;
+  const int end = (here & past) ? __ffs(here & past) - 1 : after ? 31 + __ffs(after) : 1000;
+  const bool token = p < N && my_key < none;
+  const bool is_long = token && end - first > kEmbLongGroup;
+  // The long groups that start here, one by one by the whole warp.
+  uint32_t starts = __ballot_sync(0xFFFFFFFFu, is_long && head);
+  while (starts) {
+    const int k = __ffs(starts) - 1;
+    starts &= starts - 1u;
+    const uint32_t stop = emb_group_end(ix, __shfl_sync(0xFFFFFFFFu, my_key, k), __shfl_sync(0xFFFFFFFFu, my_tok, k) / T,
+                                        p0 + k, N, T, lane);
+    if (lane == 0) ix.long_list[atomicAdd(ix.longs, 1u)] = make_uint2(static_cast<uint32_t>(p0) + k, stop);
+  }
+  if (p >= N) return;
+  ix.use[p] = (is_long ? (head ? kEmbLongSum : kEmbSkip) : kEmbRow) | (head ? kEmbHead : 0);
+  for (int c = 0; c < ix.chunks; ++c) ix.sq[static_cast<long long>(my_tok) * ix.chunks + c] = 0.0f;
+  if (!token) return;
+  if (my_row_head) {
+    ix.rows[my_key].x = static_cast<uint32_t>(p) + 1u;
+    const long long h = p + kEmbHeavyRow;
+    if (h < N && __ldcg(ix.keys + h) == my_key) ix.heavy_list[atomicAdd(ix.heavies, 1u)] = my_key;
+  }
+  // The row ends here if the next position is another row's; past the window that is looked up.
+  const bool row_ends = lane < 31 ? (row_heads >> (lane + 1)) & 1u : p + 1 >= N || __ldcg(ix.keys + p + 1) != my_key;
+  if (row_ends) ix.rows[my_key].y = static_cast<uint32_t>(p) + 1u;
+}
+
+__global__ void emb_mark_kernel(EmbIndex ix, long long N, int T_len, int V_rows) {
   griddep_enter();
-  constexpr int kWarps = kEmbSortThreads / 32;
-  __shared__ uint32_t hist[kWarps][kEmbRadix];  // counts, then each warp's next position per digit
-  __shared__ uint32_t total[kEmbRadix];         // this block's digit totals, read by the cluster
-  __shared__ uint32_t scan[kEmbRadix];
-  __shared__ uint32_t heads[2];                 // group heads in this block
-  __shared__ uint32_t warp_heads[kWarps];
+  const long long stride = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
+  for (long long w = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; w * 32 < N; w += stride)
+    emb_mark(ix, w * 32, N, static_cast<uint32_t>(T_len), static_cast<uint32_t>(V_rows), lane_id());
+}
+
+struct EmbSort {
+  const void* ids;
+  int index64;
+  long long N;
+  int V;
+  long long padding;
+  int passes;            // of 8 bits
+  uint32_t* keys[2];     // ping-pong: pass p writes [p & 1]
+  uint32_t* toks[2];
+  EmbIndex ix;           // its counters and rows are cleared here; CTAS = 1 fills the rest
+  int turns;             // counters in ix.turns
+  int T;
+  uint32_t* status;
+};
+
+// Sorts the N tokens by key in stable passes of 8 bits.  One cluster: every warp owns a contiguous
+// range of positions, in (block, warp) order, so the position of its next token of a digit is
+// (digits below) + (blocks before) + (warps before) + (its own so far), and blocks exchange only
+// their 256 digit totals, through distributed shared memory.  All of this is latency, which one
+// launch keeps smallest: with the keys of a pass held in registers, 8 blocks take about 5 us a pass
+// at 16384 tokens.  CTAS = 1 serves calls of a few thousand tokens, where a cluster's barriers would
+// cost more than its blocks save.
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 1)
+    emb_sort_kernel(const __grid_constant__ EmbSort p) {
+  griddep_enter();
+  __shared__ uint32_t hist[kEmbSortWarps][kEmbRadix];  // counts, then each warp's next position per digit
+  __shared__ uint32_t quarter[4][kEmbRadix];           // totals of 8 warps each
+  __shared__ uint32_t total[kEmbRadix];                // this block's digit totals, read by the cluster
+  __shared__ uint32_t base[kEmbRadix];
   const int tid = threadIdx.x, warp = tid / 32;
   const uint32_t lane = lane_id();
-  const uint32_t rank = cluster_rank();
-  const int gthread = static_cast<int>(rank) * kEmbSortThreads + tid;
-  constexpr int kAll = kEmbSortCtas * kEmbSortThreads;
-
-  for (long long v = gthread; v < V; v += kAll) ix.row_first[v] = 0u;
-  for (long long k = gthread; k < sq_len; k += kAll) ix.sq[k] = 0.0f;
-  if (gthread == 0) {
-    *status = 0u;
-    ix.counts[kEmbLong] = 0u;
-    ix.counts[kEmbHeavy] = 0u;
-  }
-  emb_cluster_sync();  // the status word is cleared before a key may set it
-
-  // Every warp owns one contiguous range of positions, in (block, warp) order.
-  const long long per = ((N + kEmbSortCtas * kWarps - 1) / (kEmbSortCtas * kWarps) + 31) / 32 * 32;
-  const long long w0 = (static_cast<long long>(rank) * kWarps + warp) * per;
-  const long long begin = w0 < N ? w0 : N;
-  const long long end = begin + per < N ? begin + per : N;
+  const uint32_t rank = CTAS > 1 ? cluster_rank() : 0u;
+  const int digit = tid % kEmbRadix, part = tid / kEmbRadix;
   const uint32_t below = (1u << lane) - 1u;
+  auto sync_all = [] {
+    if constexpr (CTAS > 1) {
+      __syncwarp();
+      cluster_sync_all();
+    } else {
+      __syncthreads();
+    }
+  };
 
-  for (int pass = 0; pass < passes; ++pass) {
+  const long long per = ((p.N + CTAS * kEmbSortWarps - 1) / (CTAS * kEmbSortWarps) + 31) / 32 * 32;
+  const long long w0 = (static_cast<long long>(rank) * kEmbSortWarps + warp) * per;
+  const long long begin = w0 < p.N ? w0 : p.N;
+  const long long end = begin + per < p.N ? begin + per : p.N;
+  constexpr int kHeld = 4;  // keys a thread keeps through a pass (N up to CTAS * 4096)
+  const bool held = per <= 32 * kHeld;
+
+  if (rank == 0 && tid == 0) {
+    *p.status = 0u;
+    *p.ix.heavies = 0u;
+    *p.ix.longs = 0u;
+  }
+  for (long long v = static_cast<long long>(rank) * kEmbSortThreads + tid; v < p.V; v += CTAS * kEmbSortThreads)
+    p.ix.rows[v] = make_uint2(0u, 0u);
+  for (int c = static_cast<int>(rank) * kEmbSortThreads + tid; c < p.turns; c += CTAS * kEmbSortThreads) p.ix.turns[c] = 0u;
+  sync_all();  // the status word is cleared before a key may set it
+
+  for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = 8 * pass;
-    const uint32_t* kin = ix.keys[(pass + 1) & 1];
-    const uint32_t* tin = ix.toks[(pass + 1) & 1];
-    uint32_t* kout = ix.keys[pass & 1];
-    uint32_t* tout = ix.toks[pass & 1];
-    for (int q = tid; q < kWarps * kEmbRadix; q += kEmbSortThreads) (&hist[0][0])[q] = 0u;
+    const uint32_t* kin = (pass & 1) ? p.keys[0] : p.keys[1];
+    const uint32_t* tin = (pass & 1) ? p.toks[0] : p.toks[1];
+    uint32_t* kout = (pass & 1) ? p.keys[1] : p.keys[0];
+    uint32_t* tout = (pass & 1) ? p.toks[1] : p.toks[0];
+    auto key_at = [&](long long at) {
+      return pass ? __ldcg(kin + at) : emb_key(p.ids, p.index64, at, p.V, p.padding, p.status);
+    };
+    auto tok_at = [&](long long at) { return pass ? __ldcg(tin + at) : static_cast<uint32_t>(at); };
+    uint32_t hk[kHeld], ht[kHeld];
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const long long at = begin + 32 * i + lane;
+        hk[i] = at < end ? key_at(at) : 0u;
+        ht[i] = at < end ? tok_at(at) : 0u;
+      }
+    }
+    for (int q = tid; q < kEmbSortWarps * kEmbRadix; q += kEmbSortThreads) (&hist[0][0])[q] = 0u;
     __syncthreads();
-    for (long long p = begin + lane; p < end; p += 32) {
-      const uint32_t key = pass ? __ldcg(kin + p) : emb_key(ids, index64, p, V, padding, status);
-      atomicAdd(&hist[warp][(key >> shift) & (kEmbRadix - 1)], 1u);
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (begin + 32 * i + lane < end) atomicAdd(&hist[warp][(hk[i] >> shift) & (kEmbRadix - 1)], 1u);
+    } else {
+      for (long long at = begin + lane; at < end; at += 32)
+        atomicAdd(&hist[warp][(key_at(at) >> shift) & (kEmbRadix - 1)], 1u);
     }
     __syncthreads();
-    if (tid < kEmbRadix) {
+    {  // warps before this one, among the 8 of its quarter
       uint32_t sum = 0;
-#pragma unroll 8
-      for (int w = 0; w < kWarps; ++w) {
-        const uint32_t c = hist[w][tid];
-        hist[w][tid] = sum;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const uint32_t c = hist[8 * part + w][digit];
+        hist[8 * part + w][digit] = sum;
         sum += c;
       }
-      total[tid] = sum;
-    }
-    emb_cluster_sync();
-    uint32_t before = 0, all = 0;
-    if (tid < kEmbRadix) {
-#pragma unroll
-      for (uint32_t r = 0; r < kEmbSortCtas; ++r) {
-        const uint32_t c = ld_cluster_u32(smem_addr(&total[tid]), r);
-        all += c;
-        if (r < rank) before += c;
-      }
-      scan[tid] = all;
+      quarter[part][digit] = sum;
     }
     __syncthreads();
-    // Exclusive sum of the 256 digit totals by warp 0, 8 digits a lane.
-    if (warp == 0) {
+    if (part == 0) total[digit] = quarter[0][digit] + quarter[1][digit] + quarter[2][digit] + quarter[3][digit];
+    sync_all();
+    uint32_t before = 0;
+    if (part == 0) {
+      uint32_t all = 0;
+      if constexpr (CTAS > 1) {
+#pragma unroll
+        for (uint32_t r = 0; r < CTAS; ++r) {
+          const uint32_t c = ld_cluster_u32(smem_addr(&total[digit]), r);
+          all += c;
+          if (r < rank) before += c;
+        }
+      } else {
+        all = total[digit];
+      }
+      base[digit] = all;
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive sum of the 256 digit totals, 8 digits a lane
       uint32_t c[8], sum = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         c[e] = sum;
-        sum += scan[8 * lane + e];
+        sum += base[8 * lane + e];
       }
       uint32_t run = sum;
 #pragma unroll
@@ -261,213 +391,210 @@ __global__ void __cluster_dims__(kEmbSortCtas, 1, 1) __launch_bounds__(kEmbSortT
         if (lane >= static_cast<uint32_t>(o)) run += x;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) scan[8 * lane + e] = run - sum + c[e];
+      for (int e = 0; e < 8; ++e) base[8 * lane + e] = run - sum + c[e];
     }
     __syncthreads();
-    if (tid < kEmbRadix) {
-      const uint32_t base = scan[tid] + before;
-#pragma unroll 8
-      for (int w = 0; w < kWarps; ++w) hist[w][tid] += base;
+    if (part == 0) base[digit] += before;
+    __syncthreads();
+    {
+      uint32_t b = base[digit];
+      for (int q = 0; q < part; ++q) b += quarter[q][digit];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) hist[8 * part + w][digit] += b;
     }
     __syncthreads();
-    for (long long p0 = begin; p0 < end; p0 += 32) {
-      const long long p = p0 + lane;
-      const bool ok = p < end;
-      const uint32_t key = !ok ? 0u : pass ? __ldcg(kin + p) : emb_key(ids, index64, p, V, padding, status);
-      const uint32_t tok = !ok ? 0u : pass ? __ldcg(tin + p) : static_cast<uint32_t>(p);
-      const uint32_t digit = ok ? (key >> shift) & (kEmbRadix - 1) : kEmbRadix;  // a lane without a token: no digit
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
+    auto place = [&](bool ok, uint32_t key, uint32_t tok) {
+      const uint32_t dg = ok ? (key >> shift) & (kEmbRadix - 1) : kEmbRadix;  // a lane without a token: no digit
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
       uint32_t pos = 0;
-      if (ok) pos = hist[warp][digit] + __popc(same & below);
+      if (ok) pos = hist[warp][dg] + __popc(same & below);
       __syncwarp();
-      if (ok && (same & below) == 0u) hist[warp][digit] += __popc(same);
+      if (ok && (same & below) == 0u) hist[warp][dg] += __popc(same);
       __syncwarp();
-      if (ok && DP_DCHECK(static_cast<long long>(pos) < N, 41u, status)) {
+      if (ok && DP_DCHECK(static_cast<long long>(pos) < p.N, 41u, p.status)) {
         __stcg(kout + pos, key);
         __stcg(tout + pos, tok);
       }
+    };
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (begin + 32 * i < end) place(begin + 32 * i + lane < end, hk[i], ht[i]);
+    } else {
+      for (long long at0 = begin; at0 < end; at0 += 32) {
+        const bool ok = at0 + lane < end;
+        place(ok, ok ? key_at(at0 + lane) : 0u, ok ? tok_at(at0 + lane) : 0u);
+      }
     }
-    emb_cluster_sync();  // the pass's arrays are whole, and `total` is free
+    sync_all();  // the pass's arrays are whole, and `total` is free
   }
-
-  // Group heads: a position whose id or sample differs from the one before.  Position N counts as
-  // a token of no group, so the first such position closes the last group.
-  const uint32_t* keys = ix.keys[ix.last];
-  const uint32_t* toks = ix.toks[ix.last];
-  const uint32_t none = static_cast<uint32_t>(V);
-  auto head = [&](long long p, bool& close) {
-    const uint32_t key = p < N ? __ldcg(keys + p) : none;
-    const uint32_t prev = p > 0 ? __ldcg(keys + p - 1) : none;
-    close = key == none && (p == 0 || prev != none);
-    if (key == none) return false;
-    return p == 0 || prev != key || __ldcg(toks + p - 1) / static_cast<uint32_t>(T) != __ldcg(toks + p) / static_cast<uint32_t>(T);
-  };
-  // The warp of the last token also takes position N.
-  const long long hend = (begin < N && end == N) ? N + 1 : end;
-  uint32_t mine = 0;
-  for (long long p0 = begin; p0 < hend; p0 += 32) {
-    bool close = false;
-    const bool h = p0 + lane < hend && head(p0 + lane, close);
-    mine += __popc(__ballot_sync(0xFFFFFFFFu, h));
-  }
-  if (lane == 0) warp_heads[warp] = mine;
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c = warp_heads[w];
-      warp_heads[w] = sum;
-      sum += c;
-    }
-    heads[0] = sum;
-  }
-  emb_cluster_sync();
-  if (tid == 0) {
-    uint32_t base = 0, all = 0;
-    for (uint32_t r = 0; r < kEmbSortCtas; ++r) {
-      const uint32_t c = ld_cluster_u32(smem_addr(&heads[0]), r);
-      all += c;
-      if (r < rank) base += c;
-    }
-    heads[1] = base;
-    if (rank == 0) ix.counts[kEmbGroups] = all;
-  }
-  __syncthreads();
-  uint32_t next = heads[1] + warp_heads[warp];
-  for (long long p0 = begin; p0 < hend; p0 += 32) {
-    bool close = false;
-    const bool h = p0 + lane < hend && head(p0 + lane, close);
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, h);
-    const uint32_t g = next + __popc(mask & below);
-    if ((h || close) && DP_DCHECK(static_cast<long long>(g) <= N, 42u, status))
-      __stcg(ix.group_pos + g, static_cast<uint32_t>(p0 + lane));
-    next += __popc(mask);
-  }
-  emb_cluster_sync();
-  const uint32_t groups = __ldcg(ix.counts + kEmbGroups);
-  for (uint32_t g = gthread; g < groups; g += kAll) {
-    const uint32_t p = __ldcg(ix.group_pos + g), q = __ldcg(ix.group_pos + g + 1);
-    const uint32_t key = __ldcg(keys + p);
-    int slot = -1;
-    if (q - p > kEmbLongGroup) {
-      slot = static_cast<int>(atomicAdd(ix.counts + kEmbLong, 1u));
-      ix.long_list[slot] = g;
-    }
-    ix.group_long[g] = slot;
-    if (p == 0 || __ldcg(keys + p - 1) != key) {
-      ix.row_first[key] = g + 1;
-      const long long far = static_cast<long long>(p) + kEmbHeavyRow;
-      if (far < N && __ldcg(keys + far) == key) ix.heavy_list[atomicAdd(ix.counts + kEmbHeavy, 1u)] = key;
-    }
-    if (q >= N || __ldcg(keys + q) != key) ix.row_end[key] = g + 1;
+  if constexpr (CTAS == 1) {
+    for (long long w0 = 32 * warp; w0 < p.N; w0 += 32 * kEmbSortWarps)
+      emb_mark(p.ix, w0, p.N, static_cast<uint32_t>(p.T), static_cast<uint32_t>(p.V), lane);
   }
 }
 
 // ------------------------------------------------------------------------------------- norms
-// Adds the dY rows of sorted positions p, p + step, .. below `end` to acc (this lane's vector of
-// the chunk).  The tokens of 32 rows are fetched by one load, and kU rows are in flight.
+// A chunk of a row in this kernel: kEmbVecs vectors of 16 bytes a lane.  The kernel is a stream of
+// dY rows and a warp needs bytes in flight: one sorted position a warp, one vector a lane and a
+// barrier between positions took 166 us for 8 x 2048 tokens of 4096 in bf16; this stream takes 40 with
+// two vectors and 42 with four (half the blocks fit), 134 MB at 3.4 TB/s.
+constexpr int kEmbVecs = 2;
+constexpr int kEmbWindow = 16;  // sorted positions whose groups a warp takes
+
+// blockIdx.y: chunk.  Long groups first, each by a block whose warps share its rows.  Then each warp
+// takes the short groups that start among 16 positions: these end within 32, so one load of the
+// order shows them all, and their rows are added as one stream, cut where a group ends.
 template <typename T>
-__device__ __forceinline__ void emb_add_rows(const T* __restrict__ dY, const uint32_t* __restrict__ toks,
-                                             uint32_t p, uint32_t step, uint32_t end, int d, int col, bool col_ok,
-                                             uint32_t lane, float (&acc)[EmbVec<T>::N]) {
+__global__ void __launch_bounds__(kEmbThreads, 4)
+    emb_norm_kernel(const T* __restrict__ dY, long long N, int V_rows, int d, EmbIndex ix) {
+  griddep_enter();
   constexpr int V = EmbVec<T>::N;
-  constexpr int kU = 8;
-  for (uint32_t base = p; base < end; base += 32 * step) {
-    const uint32_t at = base + lane * step;
-    const uint32_t tok = at < end ? toks[at] : 0u;
-    const int rows = static_cast<int>(min((end - base + step - 1) / step, 32u));
-    for (int k0 = 0; k0 < rows; k0 += kU) {
-      uint4 q[kU];
+  constexpr int kCols = 32 * V * kEmbVecs;
+  __shared__ float part[kEmbWarps][kCols];
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+  const int chunk = blockIdx.y, chunks = ix.chunks;
+  const int col0 = chunk * kCols + static_cast<int>(lane) * V;  // vector v of this lane: col0 + v 32 V
+  float acc[kEmbVecs][V];
+  auto clear = [&] {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const uint32_t t = __shfl_sync(0xFFFFFFFFu, tok, (k0 + u) & 31);
-        q[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (k0 + u < rows && col_ok) q[u] = __ldg(reinterpret_cast<const uint4*>(dY + static_cast<long long>(t) * d + col));
+    for (int v = 0; v < kEmbVecs; ++v)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[v][e] = 0.0f;
+  };
+  auto load = [&](uint4 (&q)[kEmbVecs], uint32_t tok, bool ok) {
+    const T* row = dY + static_cast<long long>(tok) * d + col0;
+#pragma unroll
+    for (int v = 0; v < kEmbVecs; ++v) {
+      q[v] = make_uint4(0u, 0u, 0u, 0u);
+      if (ok && col0 + v * 32 * V < d) q[v] = __ldg(reinterpret_cast<const uint4*>(row + v * 32 * V));
+    }
+  };
+  auto add = [&](const uint4 (&q)[kEmbVecs]) {
+#pragma unroll
+    for (int v = 0; v < kEmbVecs; ++v) {
+      float f[V];
+      unpack16(q[v], f, dY);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[v][e] += f[e];
+    }
+  };
+  auto squares = [&] {
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kEmbVecs; ++v)
+#pragma unroll
+      for (int e = 0; e < V; ++e) ss = fmaf(acc[v][e], acc[v][e], ss);
+    return warp_sum(ss);
+  };
+
+  const uint32_t longs = *ix.longs;
+  for (uint32_t g = blockIdx.x; g < longs; g += gridDim.x) {
+    const uint2 span = ix.long_list[g];
+    clear();
+    for (uint32_t base = span.x + warp; base < span.y; base += 32 * kEmbWarps) {
+      const uint32_t at = base + kEmbWarps * lane;
+      const uint32_t tok = at < span.y ? ix.toks[at] : 0u;
+      const int rows = static_cast<int>(min((span.y - base + kEmbWarps - 1) / kEmbWarps, 32u));
+      for (int k = 0; k < rows; k += 2) {
+        uint4 q0[kEmbVecs], q1[kEmbVecs];
+        load(q0, __shfl_sync(0xFFFFFFFFu, tok, k), true);
+        load(q1, __shfl_sync(0xFFFFFFFFu, tok, (k + 1) & 31), k + 1 < rows);
+        add(q0);
+        add(q1);
       }
+    }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (k0 + u < rows) {
-          float f[V];
-          unpack16(q[u], f, dY);
+    for (int v = 0; v < kEmbVecs; ++v)
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] += f[e];
+      for (int e = 0; e < V; ++e) part[warp][(v * V + e) * 32 + lane] = acc[v][e];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int v = 0; v < kEmbVecs; ++v)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float s = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kEmbWarps; ++w) s += part[w][(v * V + e) * 32 + lane];
+          acc[v][e] = s;
+        }
+      float* out = ix.long_sums + emb_slot(span.x) * d + col0;
+#pragma unroll
+      for (int v = 0; v < kEmbVecs; ++v) {
+        if (col0 + v * 32 * V >= d) continue;
+#pragma unroll
+        for (int e = 0; e < V / 4; ++e)
+          reinterpret_cast<float4*>(out + v * 32 * V)[e] =
+              make_float4(acc[v][4 * e], acc[v][4 * e + 1], acc[v][4 * e + 2], acc[v][4 * e + 3]);
+      }
+      const float ss = squares();
+      if (lane == 0) ix.sq[static_cast<long long>(ix.toks[span.x]) * chunks + chunk] = ss;
+    }
+    __syncthreads();
+  }
+
+  const uint32_t none = static_cast<uint32_t>(V_rows);
+  const long long windows = (N + kEmbWindow - 1) / kEmbWindow;
+  for (long long w = static_cast<long long>(blockIdx.x) * kEmbWarps + warp; w < windows;
+       w += static_cast<long long>(gridDim.x) * kEmbWarps) {
+    const long long p = w * kEmbWindow + lane;
+    const bool in = p < N;
+    const int use = in ? ix.use[p] : kEmbHead;
+    const uint32_t tok = in ? ix.toks[p] : 0u;
+    const bool row = in && (use & kEmbUseMask) == kEmbRow && ix.keys[p] != none;
+    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, (use & kEmbHead) != 0);
+    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, row);
+    if (!(heads & 0xFFFFu)) continue;
+    const int a = __ffs(heads) - 1;
+    const int z = (heads >> kEmbWindow) ? kEmbWindow + __ffs(heads >> kEmbWindow) - 1 : 32;
+    clear();
+    uint32_t first = 0;
+    for (int k = a; k < z; k += 2) {
+      uint4 q0[kEmbVecs], q1[kEmbVecs];
+      const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, tok, k), t1 = __shfl_sync(0xFFFFFFFFu, tok, (k + 1) & 31);
+      const bool r0 = (rows >> k) & 1u, r1 = k + 1 < z && ((rows >> (k + 1)) & 1u);
+      if (!r0 && !r1) continue;
+      load(q0, t0, r0);
+      load(q1, t1, r1);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = k + u;
+        if (!(u ? r1 : r0)) continue;
+        if ((heads >> at) & 1u) {
+          first = u ? t1 : t0;
+          clear();
+        }
+        add(u ? q1 : q0);
+        if (at + 1 == z || ((heads >> (at + 1)) & 1u)) {
+          const float ss = squares();
+          if (lane == 0) ix.sq[static_cast<long long>(first) * chunks + chunk] = ss;
         }
       }
     }
   }
 }
 
-// blockIdx.y: chunk of 32 vectors of 16 bytes.  Long groups first, each by a block whose warps
-// share its rows; then one group per warp.
-template <typename T>
-__global__ void __launch_bounds__(kEmbThreads) emb_norm_kernel(const T* __restrict__ dY, int d, EmbIndex ix) {
-  griddep_enter();
-  constexpr int V = EmbVec<T>::N;
-  __shared__ float part[kEmbWarps][32 * V];
-  const int warp = threadIdx.x / 32;
-  const uint32_t lane = lane_id();
-  const int chunk = blockIdx.y, chunks = gridDim.y;
-  const int col = chunk * 32 * V + static_cast<int>(lane) * V;
-  const bool col_ok = col < d;
-  const uint32_t* toks = ix.toks[ix.last];
-  const uint32_t groups = ix.counts[kEmbGroups], longs = ix.counts[kEmbLong];
-  for (uint32_t slot = blockIdx.x; slot < longs; slot += gridDim.x) {
-    const uint32_t g = ix.long_list[slot];
-    const uint32_t p = ix.group_pos[g], q = ix.group_pos[g + 1];
-    float acc[V] = {};
-    emb_add_rows(dY, toks, p + warp, kEmbWarps, q, d, col, col_ok, lane, acc);
-#pragma unroll
-    for (int e = 0; e < V; ++e) part[warp][e * 32 + lane] = acc[e];
-    __syncthreads();
-    if (warp == 0) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kEmbWarps; ++w) s += part[w][e * 32 + lane];
-        acc[e] = s;
-        ss = fmaf(s, s, ss);
-      }
-      if (col_ok) {
-        float4* out = reinterpret_cast<float4*>(ix.long_sums + static_cast<long long>(slot) * d + col);
-#pragma unroll
-        for (int e = 0; e < V / 4; ++e) out[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
-      }
-      ss = warp_sum(ss);
-      if (lane == 0) ix.sq[static_cast<long long>(toks[p]) * chunks + chunk] = ss;
-    }
-    __syncthreads();
-  }
-  for (uint32_t g = blockIdx.x * kEmbWarps + warp; g < groups; g += gridDim.x * kEmbWarps) {
-    const uint32_t p = ix.group_pos[g], q = ix.group_pos[g + 1];
-    if (q - p > kEmbLongGroup) continue;
-    float acc[V] = {};
-    emb_add_rows(dY, toks, p, 1u, q, d, col, col_ok, lane, acc);
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) ss = fmaf(acc[e], acc[e], ss);
-    ss = warp_sum(ss);
-    if (lane == 0) ix.sq[static_cast<long long>(toks[p]) * chunks + chunk] = ss;
-  }
-}
-
 // norms[i] = |scale| sqrt(sum of the sample's T * chunks slots): one block a sample, fp64, in a
 // fixed order.
-__global__ void emb_norms_kernel(const float* __restrict__ sq, long long per_sample, float scale,
-                                 float* __restrict__ norms, float* __restrict__ norms_out) {
+constexpr int kEmbNormThreads = 512;
+__global__ void __launch_bounds__(kEmbNormThreads)
+    emb_norms_kernel(const float* __restrict__ sq, long long per_sample, float scale, float* __restrict__ norms,
+                     float* __restrict__ norms_out) {
   griddep_enter();
-  __shared__ double part[kEmbWarps];
+  __shared__ double part[kEmbNormThreads / 32];
   const float* mine = sq + static_cast<long long>(blockIdx.x) * per_sample;
   double acc = 0.0;
-  for (long long k = threadIdx.x; k < per_sample; k += kEmbThreads) acc += static_cast<double>(mine[k]);
+#pragma unroll 8
+  for (long long k = threadIdx.x; k < per_sample; k += kEmbNormThreads) acc += static_cast<double>(mine[k]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
     double s = 0.0;
-    for (int w = 0; w < kEmbWarps; ++w) s += part[w];
+    for (int w = 0; w < kEmbNormThreads / 32; ++w) s += part[w];
     const float n = static_cast<float>(fabs(static_cast<double>(scale)) * sqrt(s));
     if (norms) norms[blockIdx.x] = n;
     if (norms_out) norms_out[blockIdx.x] = n;
@@ -475,114 +602,156 @@ __global__ void emb_norms_kernel(const float* __restrict__ sq, long long per_sam
 }
 
 // --------------------------------------------------------------------------------------- sum
-// acc += sum over groups first, first + step, .. below `end` of scale c_i (group's sum).
+// A lane's 16 bytes of a dY row as quads of columns.
 template <typename T>
-__device__ __forceinline__ void emb_add_groups(const T* __restrict__ dY, const EmbIndex& ix, uint32_t first,
-                                               uint32_t step, uint32_t end, int T_len, const float* __restrict__ norms,
-                                               float C, float scale, int d, int col, bool col_ok, uint32_t lane,
-                                               float (&acc)[EmbVec<T>::N]) {
-  constexpr int V = EmbVec<T>::N;
-  const uint32_t* toks = ix.toks[ix.last];
-  for (uint32_t g = first; g < end; g += step) {
-    const uint32_t p = ix.group_pos[g], q = ix.group_pos[g + 1];
-    const int slot = ix.group_long[g];
-    const float w = scale * clip_factor(norms[toks[p] / static_cast<uint32_t>(T_len)], C);
-    float s[V] = {};
-    if (slot >= 0) {
-      if (col_ok) {
-        const float4* in = reinterpret_cast<const float4*>(ix.long_sums + static_cast<long long>(slot) * d + col);
+constexpr int kEmbQuads = EmbVec<T>::N / 4;
+
+__device__ __forceinline__ float4 fma4(float c, float4 x, float4 a) {
+  return make_float4(fmaf(c, x.x, a.x), fmaf(c, x.y, a.y), fmaf(c, x.z, a.z), fmaf(c, x.w, a.w));
+}
+
+// acc += scale c_i (token's row, or long group's sum) over the sorted positions first .. end.
+template <typename T>
+__device__ __forceinline__ void emb_add_clipped(const T* __restrict__ dY, const EmbIndex& ix, uint32_t first,
+                                                uint32_t end, uint32_t T_len, const float* __restrict__ norms, float C,
+                                                float scale, int d, int col, uint32_t lane, float4 (&acc)[kEmbQuads<T>]) {
+  constexpr int Q = kEmbQuads<T>;
+  constexpr int kU = 4;
+  for (uint32_t base = first; base < end; base += 32) {
+    const uint32_t at = base + lane;
+    const bool in = at < end;
+    const uint32_t tok = in ? ix.toks[at] : 0u;
+    const int use = in ? ix.use[at] & kEmbUseMask : kEmbSkip;
+    const float w = in ? scale * clip_factor(norms[tok / T_len], C) : 0.0f;
+    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, use == kEmbRow);
+    uint32_t longs = __ballot_sync(0xFFFFFFFFu, use == kEmbLongSum);
+    const int count = static_cast<int>(end - base < 32u ? end - base : 32u);
+    for (int k0 = 0; k0 < count; k0 += kU) {
+      if (!((rows >> k0) & ((1u << kU) - 1u))) continue;
+      uint4 q[kU];
 #pragma unroll
-        for (int e = 0; e < V / 4; ++e) {
-          const float4 x = in[e];
-          s[4 * e] = x.x;
-          s[4 * e + 1] = x.y;
-          s[4 * e + 2] = x.z;
-          s[4 * e + 3] = x.w;
-        }
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t t = __shfl_sync(0xFFFFFFFFu, tok, k0 + u);
+        q[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (((rows >> (k0 + u)) & 1u) && col < d)
+          q[u] = __ldg(reinterpret_cast<const uint4*>(dY + static_cast<long long>(t) * d + col));
       }
-    } else {
-      emb_add_rows(dY, toks, p, 1u, q, d, col, col_ok, lane, s);
-    }
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, s[e], acc[e]);
+      for (int u = 0; u < kU; ++u) {
+        const float c = __shfl_sync(0xFFFFFFFFu, w, k0 + u);
+        if (!((rows >> (k0 + u)) & 1u)) continue;
+        float f[4 * Q];
+        unpack16(q[u], f, dY);
+#pragma unroll
+        for (int e = 0; e < Q; ++e) acc[e] = fma4(c, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]), acc[e]);
+      }
+    }
+    while (longs) {
+      const int k = __ffs(longs) - 1;
+      longs &= longs - 1u;
+      const float c = __shfl_sync(0xFFFFFFFFu, w, k);
+      if (col >= d) continue;
+      const float4* sum = reinterpret_cast<const float4*>(ix.long_sums + emb_slot(base + k) * d + col);
+#pragma unroll
+      for (int e = 0; e < Q; ++e) acc[e] = fma4(c, sum[e], acc[e]);
+    }
   }
 }
 
-// S[v, :] (+)= its groups' clipped sums + std z, blockIdx.y: chunk as above.  Heavy rows first,
-// each by a block; then one row per warp.  ACCUMULATE: rows that occur are added to, the others
-// left alone.  NOISE: Box-Muller tables in shared memory; the normals' fp64 arithmetic is then what
-// bounds the kernel (2 fp64 pipes' worth a pair), the stores otherwise.
+// S[v, :] (+)= its tokens' clipped sums + std z, blockIdx.y: chunk of 32 vectors of 16 bytes.  Heavy
+// rows first, each by a block whose warps share its positions; then one row per warp, handed out by
+// the chunk's counter (a fixed split left 10% of the SMs' time idle behind the blocks with heavy
+// rows).  ACCUMULATE: rows that occur are added to, the others left alone.
+// NOISE: Box-Muller tables in shared memory; the normals' arithmetic is then what bounds the
+// kernel, the stores of S otherwise.
 template <typename T, bool NOISE, bool ACCUMULATE>
-__global__ void __launch_bounds__(kEmbThreads)
+__global__ void __launch_bounds__(kEmbThreads, NOISE ? 4 : 3)
     emb_sum_kernel(const T* __restrict__ dY, EmbIndex ix, int T_len, int V_rows, int d, const float* __restrict__ norms,
                    float C, float scale, double noise_std, PhiloxKey key, uint32_t layer_id, StepRef step,
                    float* __restrict__ S) {
   griddep_enter();
-  constexpr int V = EmbVec<T>::N;
-  __shared__ float part[kEmbWarps][32 * V];
+  constexpr int Q = kEmbQuads<T>;
+  __shared__ float4 part[kEmbWarps][32 * Q];
   __shared__ double2 tab_s[NOISE ? kNoiseSharedEntries : 1];
   if constexpr (NOISE) stage_noise_tables(tab_s);
   __syncthreads();
   const uint32_t step_lo = NOISE ? step.get() : 0u;
   const int warp = threadIdx.x / 32;
   const uint32_t lane = lane_id();
-  const int col = blockIdx.y * 32 * V + static_cast<int>(lane) * V;
-  const bool col_ok = col < d;
-  auto store = [&](long long v, float (&acc)[V]) {
-    if (!col_ok || !DP_DCHECK(in_buffer(v * d + col, V, static_cast<long long>(V_rows) * d), 43u, nullptr)) return;
-    float4* out = reinterpret_cast<float4*>(S + v * d + col);
+  const int col = (blockIdx.y * 32 + static_cast<int>(lane)) * 4 * Q;
+  auto store = [&](long long v, float4 (&acc)[Q]) {
+    const long long at = v * d + col;
+    if constexpr (NOISE) {
+      // All quads' normals without a branch between them: their chains interleave.
 #pragma unroll
-    for (int e = 0; e < V / 4; ++e) {
-      float4 x = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
-      if constexpr (NOISE) {
+      for (int e = 0; e < Q; ++e) {
         double z[4];
-        normals4(static_cast<uint32_t>((static_cast<unsigned long long>(v) * d + col) / 4 + e), layer_id, step_lo,
-                 kStreamNoise, key, z, NoiseTablesShared{tab_s}, noise_std);
-        x.x = static_cast<float>(static_cast<double>(x.x) + z[0]);
-        x.y = static_cast<float>(static_cast<double>(x.y) + z[1]);
-        x.z = static_cast<float>(static_cast<double>(x.z) + z[2]);
-        x.w = static_cast<float>(static_cast<double>(x.w) + z[3]);
+        normals4(static_cast<uint32_t>(static_cast<unsigned long long>(at) / 4) + e, layer_id, step_lo, kStreamNoise,
+                 key, z, NoiseTablesShared{tab_s}, noise_std);
+        acc[e].x = static_cast<float>(static_cast<double>(acc[e].x) + z[0]);
+        acc[e].y = static_cast<float>(static_cast<double>(acc[e].y) + z[1]);
+        acc[e].z = static_cast<float>(static_cast<double>(acc[e].z) + z[2]);
+        acc[e].w = static_cast<float>(static_cast<double>(acc[e].w) + z[3]);
       }
-      if constexpr (ACCUMULATE) {
-        const float4 o = out[e];
-        x = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-      }
-      out[e] = x;
+    }
+    if (col >= d || !DP_DCHECK(in_buffer(at, 4 * Q, static_cast<long long>(V_rows) * d), 43u, nullptr)) return;
+    float4* out = reinterpret_cast<float4*>(S + at);
+#pragma unroll
+    for (int e = 0; e < Q; ++e) {
+      if constexpr (ACCUMULATE) acc[e] = fma4(1.0f, out[e], acc[e]);
+      out[e] = acc[e];
     }
   };
-  const uint32_t heavy = ix.counts[kEmbHeavy];
+  const uint32_t heavy = *ix.heavies;
   for (uint32_t h = blockIdx.x; h < heavy; h += gridDim.x) {
     const uint32_t v = ix.heavy_list[h];
-    const uint32_t first = ix.row_first[v] - 1, end = ix.row_end[v];
-    float acc[V] = {};
-    emb_add_groups(dY, ix, first + warp, kEmbWarps, end, T_len, norms, C, scale, d, col, col_ok, lane, acc);
+    const uint2 row = ix.rows[v];
+    const uint32_t share = (row.y - row.x + kEmbWarps) / kEmbWarps;  // (positions + warps - 1) / warps
+    const uint32_t first = row.x - 1u + share * warp;
+    float4 acc[Q] = {};
+    emb_add_clipped(dY, ix, first, min(first + share, row.y), static_cast<uint32_t>(T_len), norms, C, scale, d, col, lane,
+                    acc);
 #pragma unroll
-    for (int e = 0; e < V; ++e) part[warp][e * 32 + lane] = acc[e];
+    for (int e = 0; e < Q; ++e) part[warp][e * 32 + lane] = acc[e];
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float s = 0.0f;
+      for (int e = 0; e < Q; ++e) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kEmbWarps; ++w) s += part[w][e * 32 + lane];
+        for (int w = 0; w < kEmbWarps; ++w) s = fma4(1.0f, part[w][e * 32 + lane], s);
         acc[e] = s;
       }
       store(v, acc);
     }
     __syncthreads();
   }
-  for (long long v = static_cast<long long>(blockIdx.x) * kEmbWarps + warp; v < V_rows;
-       v += static_cast<long long>(gridDim.x) * kEmbWarps) {
-    const uint32_t first = ix.row_first[v];
-    float acc[V] = {};
-    if (first) {
-      const uint32_t end = ix.row_end[v];
-      if (ix.group_pos[end] - ix.group_pos[first - 1] > kEmbHeavyRow) continue;
-      emb_add_groups(dY, ix, first - 1, 1u, end, T_len, norms, C, scale, d, col, col_ok, lane, acc);
-    } else if (ACCUMULATE) {
-      continue;
+  // A turn is up to 8 rows, `turns` apart: ids near each other are often alike in frequency (common
+  // ones first), and a warp that took 8 neighbours would have all the long rows.
+  const long long warps = static_cast<long long>(gridDim.x) * kEmbWarps;
+  // At least two turns a warp; fewer rows a turn would queue on the counter (50257 turns took 100 us).
+  const long long share = V_rows / (2 * warps);
+  const int count = share < 1 ? 1 : share > 8 ? 8 : static_cast<int>(share);
+  const long long turns = (V_rows + count - 1) / count;
+  for (;;) {
+    uint32_t turn = lane == 0 ? atomicAdd(ix.turns + blockIdx.y, 1u) : 0u;
+    turn = __shfl_sync(0xFFFFFFFFu, turn, 0);
+    if (turn >= turns) break;
+    const long long mine = turn + lane * turns;
+    const uint2 entry = lane < count && mine < V_rows ? ix.rows[mine] : make_uint2(0u, 0u);
+    for (int k = 0; k < count; ++k) {
+      const long long v = turn + k * turns;
+      if (v >= V_rows) break;
+      const uint32_t first = __shfl_sync(0xFFFFFFFFu, entry.x, k), end = __shfl_sync(0xFFFFFFFFu, entry.y, k);
+      float4 acc[Q] = {};
+      if (first) {
+        if (end - first >= kEmbHeavyRow) continue;  // end - (first - 1) tokens: more than kEmbHeavyRow
+        emb_add_clipped(dY, ix, first - 1u, end, static_cast<uint32_t>(T_len), norms, C, scale, d, col, lane, acc);
+      } else if (ACCUMULATE) {
+        continue;
+      }
+      store(v, acc);
     }
-    store(v, acc);
   }
 }
 

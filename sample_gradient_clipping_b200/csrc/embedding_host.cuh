@@ -9,7 +9,8 @@ struct EmbCall {
   dp_dtype dt;
   long long N() const { return static_cast<long long>(B) * T; }
   int vec() const { return dt == DP_BF16 ? 8 : 4; }
-  int chunks() const { return ceil_div(d, 32 * vec()); }
+  int chunks() const { return ceil_div(d, 32 * vec()); }                       // of the sum kernel
+  int norm_chunks() const { return ceil_div(d, 32 * vec() * kEmbVecs); }  // of the norm kernel
 };
 
 bool valid_index(dp_index it) { return it == DP_I32 || it == DP_I64; }
@@ -23,11 +24,11 @@ bool valid_embedding(const EmbCall& s) {
 }
 
 struct EmbLayout {
-  size_t keys[2], toks[2], row_first, row_end, group_pos, group_long, long_list, heavy_list, sq, long_sums, norms, total;
+  size_t keys[2], toks[2], rows, use, heavy_list, long_list, turns, sq, long_sums, norms, total;
 };
 
-// The counters share the status word's 256 bytes.
-constexpr size_t kEmbCountsOffset = 128;
+// The counts of heavy rows and long groups share the status word's 256 bytes.
+constexpr size_t kEmbHeaviesOffset = 128, kEmbLongsOffset = 132;
 
 EmbLayout emb_layout(const EmbCall& s) {
   EmbLayout L{};
@@ -38,19 +39,17 @@ EmbLayout emb_layout(const EmbCall& s) {
     return o;
   };
   const size_t N = static_cast<size_t>(s.N());
-  const size_t longs = N / (kEmbLongGroup + 1) + 1;  // a long group has at least kEmbLongGroup + 1 tokens
   for (int k = 0; k < 2; ++k) {
     L.keys[k] = take(N * 4);
     L.toks[k] = take(N * 4);
   }
-  L.row_first = take(static_cast<size_t>(s.V) * 4);
-  L.row_end = take(static_cast<size_t>(s.V) * 4);
-  L.group_pos = take((N + 1) * 4);
-  L.group_long = take(N * 4);
-  L.long_list = take(longs * 4);
-  L.heavy_list = take((N / (kEmbHeavyRow + 1) + 1) * 4);
-  L.sq = take(N * s.chunks() * 4);
-  L.long_sums = take(longs * s.d * 4);
+  L.rows = take(static_cast<size_t>(s.V) * sizeof(uint2));
+  L.use = take(N);
+  L.heavy_list = take((N / (kEmbHeavyRow + 1) + 1) * 4);  // a heavy row has at least kEmbHeavyRow + 1 tokens
+  L.long_list = take(static_cast<size_t>(emb_slot(s.N()) + 1) * sizeof(uint2));
+  L.turns = take(static_cast<size_t>(s.chunks()) * 4);
+  L.sq = take(N * s.norm_chunks() * 4);
+  L.long_sums = take(static_cast<size_t>(emb_slot(s.N()) + 1) * s.d * 4);
   L.norms = take(static_cast<size_t>(s.B) * 4);
   L.total = at;
   return L;
@@ -59,49 +58,74 @@ EmbLayout emb_layout(const EmbCall& s) {
 EmbIndex emb_index(const EmbCall& s, const EmbLayout& L, uint8_t* ws, int passes) {
   auto u32 = [&](size_t o) { return reinterpret_cast<uint32_t*>(ws + o); };
   EmbIndex ix{};
-  for (int k = 0; k < 2; ++k) {
-    ix.keys[k] = u32(L.keys[k]);
-    ix.toks[k] = u32(L.toks[k]);
-  }
-  ix.last = (passes - 1) & 1;
-  ix.counts = u32(kEmbCountsOffset);
-  ix.row_first = u32(L.row_first);
-  ix.row_end = u32(L.row_end);
-  ix.group_pos = u32(L.group_pos);
-  ix.group_long = reinterpret_cast<int*>(ws + L.group_long);
-  ix.long_list = u32(L.long_list);
+  const int last = (passes - 1) & 1;
+  ix.keys = u32(L.keys[last]);
+  ix.toks = u32(L.toks[last]);
+  ix.heavies = u32(kEmbHeaviesOffset);
   ix.heavy_list = u32(L.heavy_list);
+  ix.longs = u32(kEmbLongsOffset);
+  ix.long_list = reinterpret_cast<uint2*>(ws + L.long_list);
+  ix.turns = u32(L.turns);
+  ix.chunks = s.norm_chunks();
+  ix.rows = reinterpret_cast<uint2*>(ws + L.rows);
+  ix.use = ws + L.use;
   ix.sq = reinterpret_cast<float*>(ws + L.sq);
   ix.long_sums = reinterpret_cast<float*>(ws + L.long_sums);
-  (void)s;
   return ix;
 }
 
-// Grid of the norm and sum kernels: x over groups or rows, y over chunks, `per_sm` blocks an SM.
-dim3 emb_grid(const EmbCall& s, long long items, int per_sm) {
-  const long long want = static_cast<long long>(sm_count()) * per_sm / s.chunks();
+// Up to this many tokens one block sorts them.
+constexpr long long kEmbSortAlone = 4096;
+
+// Grid of the norm and sum kernels: x over warps' items, y over chunks, `per_sm` blocks an SM.
+dim3 emb_grid(int chunks, long long items, int per_sm) {
+  const long long want = static_cast<long long>(sm_count()) * per_sm / chunks;
   const long long most = (items + kEmbWarps - 1) / kEmbWarps;
   const long long x = std::max(1ll, std::min(want, most));
-  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(s.chunks()));
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(chunks));
 }
 
-dp_status emb_sort(const EmbCall& s, const EmbIndex& ix, int passes, const void* ids, dp_index it, long long padding,
-                   bool sums_squares, uint32_t* status, cudaStream_t stream) {
+dp_status emb_sort(const EmbCall& s, const EmbLayout& L, const EmbIndex& ix, int passes, const void* ids, dp_index it, long long padding,
+                   uint8_t* ws, cudaStream_t stream) {
+  EmbSort p{};
+  p.ids = ids;
+  p.index64 = it == DP_I64 ? 1 : 0;
+  p.N = s.N();
+  p.V = s.V;
+  p.padding = padding;
+  p.passes = passes;
+  for (int k = 0; k < 2; ++k) {
+    p.keys[k] = reinterpret_cast<uint32_t*>(ws + L.keys[k]);
+    p.toks[k] = reinterpret_cast<uint32_t*>(ws + L.toks[k]);
+  }
+  p.ix = ix;
+  p.turns = s.chunks();
+  p.T = s.T;
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  if (p.N <= kEmbSortAlone) {
+    LaunchScope scope(kKindEmbSort, stream);
+    DP_LAUNCH("emb_sort_kernel", emb_sort_kernel<1>, 1, kEmbSortThreads, 0, stream, p);
+    return DP_OK;
+  }
+  {
+    LaunchScope scope(kKindEmbSort, stream);
+    DP_LAUNCH("emb_sort_kernel", emb_sort_kernel<8>, 8, kEmbSortThreads, 0, stream, p);
+  }
   LaunchScope scope(kKindEmbSort, stream);
-  DP_LAUNCH("emb_sort_kernel", emb_sort_kernel, kEmbSortCtas, kEmbSortThreads, 0, stream, ids, it == DP_I64 ? 1 : 0,
-            s.N(), s.T, s.V, padding, passes, ix, sums_squares ? s.N() * s.chunks() : 0ll, status);
+  DP_LAUNCH("emb_mark_kernel", emb_mark_kernel, stream_grid(static_cast<unsigned long long>(p.N), 128), 128, 0, stream, ix,
+            p.N, s.T, s.V);
   return DP_OK;
 }
 
 dp_status emb_group_sums(const EmbCall& s, const EmbIndex& ix, const void* dY, cudaStream_t stream) {
-  const dim3 grid = emb_grid(s, s.N(), 8);
+  const dim3 grid = emb_grid(s.norm_chunks(), (s.N() + kEmbWindow - 1) / kEmbWindow, 8);
   LaunchScope scope(kKindEmbNorm, stream);
   if (s.dt == DP_BF16) {
     DP_LAUNCH("emb_norm_kernel", emb_norm_kernel<__nv_bfloat16>, grid, kEmbThreads, 0, stream,
-              static_cast<const __nv_bfloat16*>(dY), s.d, ix);
+              static_cast<const __nv_bfloat16*>(dY), s.N(), s.V, s.d, ix);
   } else {
     DP_LAUNCH("emb_norm_kernel", emb_norm_kernel<float>, grid, kEmbThreads, 0, stream, static_cast<const float*>(dY),
-              s.d, ix);
+              s.N(), s.V, s.d, ix);
   }
   return DP_OK;
 }
@@ -109,8 +133,8 @@ dp_status emb_group_sums(const EmbCall& s, const EmbIndex& ix, const void* dY, c
 dp_status emb_norms(const EmbCall& s, const EmbIndex& ix, float scale, float* norms, float* norms_out,
                     cudaStream_t stream) {
   LaunchScope scope(kKindFinalize, stream);
-  DP_LAUNCH("emb_norms_kernel", emb_norms_kernel, s.B, kEmbThreads, 0, stream, ix.sq,
-            static_cast<long long>(s.T) * s.chunks(), scale, norms, norms_out);
+  DP_LAUNCH("emb_norms_kernel", emb_norms_kernel, s.B, kEmbNormThreads, 0, stream, ix.sq,
+            static_cast<long long>(s.T) * s.norm_chunks(), scale, norms, norms_out);
   return DP_OK;
 }
 
@@ -121,13 +145,13 @@ dp_status emb_sum_as(const EmbCall& s, const EmbIndex& ix, const T* dY, const fl
   const PhiloxKey key = philox_key_from_seed(seed);
   LaunchScope scope(kKindEmbSum, stream);
   if (accumulate) {
-    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, true>), emb_grid(s, s.V, 8), kEmbThreads, 0, stream, dY, ix,
+    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, true>), emb_grid(s.chunks(), s.V, 8), kEmbThreads, 0, stream, dY, ix,
               s.T, s.V, s.d, norms, C, scale, 0.0, key, layer_id, step, S);
   } else if (noise_std != 0.0) {
-    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, true, false>), emb_grid(s, s.V, 4), kEmbThreads, 0, stream, dY, ix,
+    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, true, false>), emb_grid(s.chunks(), s.V, 4), kEmbThreads, 0, stream, dY, ix,
               s.T, s.V, s.d, norms, C, scale, noise_std, key, layer_id, step, S);
   } else {
-    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, false>), emb_grid(s, s.V, 8), kEmbThreads, 0, stream, dY, ix,
+    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, false>), emb_grid(s.chunks(), s.V, 8), kEmbThreads, 0, stream, dY, ix,
               s.T, s.V, s.d, norms, C, scale, 0.0, key, layer_id, step, S);
   }
   return DP_OK;
@@ -195,7 +219,7 @@ dp_status embedding_step(const void* ids, dp_index it, const void* dY, dp_dtype 
   const EmbIndex ix = emb_index(s, L, ws, passes);
   float* norms = reinterpret_cast<float*>(ws + L.norms);
   const double noise_std = (sigma == 0.0f) ? 0.0 : static_cast<double>(sigma) * static_cast<double>(C);
-  if ((st = emb_sort(s, ix, passes, ids, it, padding_idx, true, reinterpret_cast<uint32_t*>(ws), cs)) != DP_OK) return st;
+  if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
   if ((st = emb_group_sums(s, ix, dY, cs)) != DP_OK) return st;
   if ((st = emb_norms(s, ix, scale, norms, norms_out, cs)) != DP_OK) return st;
   return emb_sum(s, ix, dY, norms, C, scale, false, noise_std, seed, step, layer_id, G_out, cs);
@@ -240,7 +264,7 @@ dp_status dp_embedding_per_sample_norms(const void* ids, dp_index it, const void
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const EmbIndex ix = emb_index(s, L, ws, passes);
-  if ((st = emb_sort(s, ix, passes, ids, it, padding_idx, true, reinterpret_cast<uint32_t*>(ws), cs)) != DP_OK) return st;
+  if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
   if ((st = emb_group_sums(s, ix, dY, cs)) != DP_OK) return st;
   return emb_norms(s, ix, scale, nullptr, norms, cs);
 }
@@ -258,7 +282,7 @@ dp_status dp_embedding_clip_accumulate(const void* ids, dp_index it, const void*
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const EmbIndex ix = emb_index(s, L, ws, passes);
-  if ((st = emb_sort(s, ix, passes, ids, it, padding_idx, true, reinterpret_cast<uint32_t*>(ws), cs)) != DP_OK) return st;
+  if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
   // The long groups' sums are the norm kernel's; the norms themselves are the caller's.
   if ((st = emb_group_sums(s, ix, dY, cs)) != DP_OK) return st;
   return emb_sum(s, ix, dY, norms, C, scale, true, 0.0, 0, step_value(0), 0, G_sum, cs);

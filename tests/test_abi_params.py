@@ -74,8 +74,8 @@ def test_embedding_workspace_size(L):
     f = L.dp_embedding_workspace_size
     N, V, d = 8 * 2048, 32000, 4096
     longs = N // 17 + 1                                   # fp32 sums of groups of more than 16 tokens
-    want = 4 * N * 6 + 8 * V + N * 16 * 4 + longs * d * 4
-    assert want <= f(8, 2048, V, d, BF16) < want + 8192 + 4 * N // 8
+    want = N * 17 + 8 * V + N * 8 * 4 + longs * (d * 4 + 8)
+    assert want <= f(8, 2048, V, d, BF16) < want + 8192
     assert f(8, 2048, V, 12, BF16) == 0 and f(8, 2048, V, 12, F32) > 0 and f(0, 1, 1, 8, BF16) == 0
 
 
