@@ -20,17 +20,21 @@ dp_status check_norm_shape(const NormCall& s) {
   return s.vecs() > kNormMaxVecs ? DP_ERR_UNSUPPORTED : DP_OK;
 }
 
-// Threads of a row in the backward, and how many blocks of that size it is cut for on 148 SMs.
-int norm_row_threads(const NormCall& s) {
-  const int v = s.vecs();
-  return v <= 128 ? 32 : v <= 512 ? 128 : v <= 1024 ? 256 : 512;
+// The backward's blocks: up to 512 threads, one row at a time.
+int norm_threads(const NormCall& s) { return std::min(512, ceil_div(s.vecs(), 32) * 32); }
+
+// Blocks that share an SM: 1024 threads (the kernel's registers allow that many with one vector a
+// thread, 512 with more), while two slots each of the three tensors' rows fit in shared memory.
+constexpr int kNormRingBytes = 216 * 1024;
+int norm_blocks_per_sm(const NormCall& s) {
+  const int threads = norm_threads(s);
+  const int by_threads = s.vecs() > threads ? 1 : std::min(16, 1024 / threads);
+  return std::max(1, std::min(by_threads, kNormRingBytes / (2 * 3 * s.vecs() * 16)));
 }
 
 // Parts of a sample in the backward: blocks fill 148 SMs, each part a run of rows.
 int norm_parts(const NormCall& s) {
-  const int tpr = norm_row_threads(s);
-  const int per_sm = tpr == 32 ? 16 : tpr == 128 ? 4 : tpr == 256 ? 2 : 1;
-  const long long want = std::max(1, 148 * per_sm / s.B);
+  const long long want = std::max(1, 148 * norm_blocks_per_sm(s) / s.B);
   const int per = static_cast<int>((s.T + want - 1) / want);
   return ceil_div(s.T, per);
 }
@@ -78,35 +82,40 @@ dp_status rmsnorm_as(const NormCall& s, long long rows, const void* X, const voi
   return rmsnorm_launch<T, 512, 4>(s, rows, X, res, gain, eps, H, Y, stream);
 }
 
-template <typename T, int TPR, int NV>
+template <typename T, int NV, bool RES>
 dp_status rmsnorm_backward_launch(const NormCall& s, const void* H, const float* gain, const void* dY, const void* dres,
                                   float eps, void* dX, float* parts, uint32_t* status, cudaStream_t stream) {
+  constexpr int tensors = RES ? 3 : 2;
   const int nparts = norm_parts(s);
   const int per = ceil_div(s.T, nparts);
+  const int slot = tensors * s.vecs() * 16;
+  const int stages = std::max(2, std::min({kNormStagesMax, per, kNormRingBytes / norm_blocks_per_sm(s) / slot}));
+  static std::atomic<bool> configured[64] = {};
+  int dev = 0;
+  DP_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+    DP_CUDA(cudaFuncSetAttribute(rmsnorm_backward_kernel<T, NV, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kNormRingBytes));
+    if (dev >= 0 && dev < 64) configured[dev].store(true);
+  }
   const dim3 grid(static_cast<unsigned>(nparts), static_cast<unsigned>(s.B));
   LaunchScope scope(kKindRmsNormBackward, stream);
-  if (dres) {
-    DP_LAUNCH("rmsnorm_backward_kernel", (rmsnorm_backward_kernel<T, TPR, NV, true>), grid, TPR, 0, stream,
-              static_cast<const T*>(H), gain, static_cast<const T*>(dY), static_cast<const T*>(dres), s.T, s.d, eps, per,
-              static_cast<T*>(dX), parts, status);
-  } else {
-    DP_LAUNCH("rmsnorm_backward_kernel", (rmsnorm_backward_kernel<T, TPR, NV, false>), grid, TPR, 0, stream,
-              static_cast<const T*>(H), gain, static_cast<const T*>(dY), static_cast<const T*>(dres), s.T, s.d, eps, per,
-              static_cast<T*>(dX), parts, status);
-  }
+  DP_LAUNCH("rmsnorm_backward_kernel", (rmsnorm_backward_kernel<T, NV, RES>), grid, norm_threads(s),
+            static_cast<size_t>(stages) * slot, stream, static_cast<const T*>(H), gain, static_cast<const T*>(dY),
+            static_cast<const T*>(dres), s.T, s.d, eps, per, stages, static_cast<T*>(dX), parts, status);
   return DP_OK;
 }
 
 template <typename T>
 dp_status rmsnorm_backward_as(const NormCall& s, const void* H, const float* gain, const void* dY, const void* dres,
                               float eps, void* dX, float* parts, uint32_t* status, cudaStream_t stream) {
-  const int v = s.vecs();
-  if (v <= 32) return rmsnorm_backward_launch<T, 32, 1>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
-  if (v <= 128) return rmsnorm_backward_launch<T, 32, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
-  if (v <= 256) return rmsnorm_backward_launch<T, 128, 2>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
-  if (v <= 512) return rmsnorm_backward_launch<T, 128, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
-  if (v <= 1024) return rmsnorm_backward_launch<T, 256, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
-  return rmsnorm_backward_launch<T, 512, 4>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  auto run = [&](auto launch_res, auto launch) {
+    return dres ? launch_res(s, H, gain, dY, dres, eps, dX, parts, status, stream)
+                : launch(s, H, gain, dY, dres, eps, dX, parts, status, stream);
+  };
+  if (s.vecs() <= 512) return run(rmsnorm_backward_launch<T, 1, true>, rmsnorm_backward_launch<T, 1, false>);
+  if (s.vecs() <= 1024) return run(rmsnorm_backward_launch<T, 2, true>, rmsnorm_backward_launch<T, 2, false>);
+  return run(rmsnorm_backward_launch<T, 4, true>, rmsnorm_backward_launch<T, 4, false>);
 }
 
 dp_status check_norm_backward(const NormCall& s, const void* H, const float* gain, const void* dY, const void* dres,
