@@ -62,22 +62,34 @@ cudaError_t injected_launch_error() {
   return static_cast<cudaError_t>(g_inject_error.load());
 }
 
+// `cluster` > 1: CTAs of a cluster along x, for a kernel without compile-time cluster dimensions
+// (0: none, or the kernel's own).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t stream, Args&&... args) {
+cudaError_t launch_kernel_cluster(int cluster, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                  cudaStream_t stream, Args&&... args) {
   const cudaError_t injected = injected_launch_error();
   if (injected != cudaSuccess) return injected;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster > 0 ? static_cast<unsigned>(cluster) : 1u;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, Args&&... args) {
+  return launch_kernel_cluster(0, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 #define DP_LAUNCH(what, ...)                             \
@@ -85,6 +97,13 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
     cudaError_t e_ = launch_kernel(__VA_ARGS__);         \
     if (e_ == cudaSuccess) e_ = cudaGetLastError();      \
     if (e_ != cudaSuccess) return cuda_fail(e_, what);   \
+  } while (0)
+
+#define DP_LAUNCH_CLUSTER(what, cluster, ...)                      \
+  do {                                                             \
+    cudaError_t e_ = launch_kernel_cluster(cluster, __VA_ARGS__);  \
+    if (e_ == cudaSuccess) e_ = cudaGetLastError();                \
+    if (e_ != cudaSuccess) return cuda_fail(e_, what);             \
   } while (0)
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -467,6 +467,338 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   ns_body<Cfg>(p);
 }
 
+// ------------------------------------------------------------------------ one launch, m <= 128
+// The whole iteration of a matrix with at most 128 rows (as m x n), such as a projected gradient of
+// r = 128, in one cluster.  Every CTA keeps up to 256 columns of X: in fp32 in TMEM, and their fp16
+// part as a shared-memory tile that serves both products (K-major for X X^T, MN-major for B X).  A step:
+//   each CTA forms X X^T of its columns; the CTAs add their parts (each the rows it owns, sent as
+//   columns: the matrix is symmetric, and so a warp's 32 lanes write 128 contiguous bytes) and send the
+//   rounded rows of A to all; each forms B, and then its columns of the next X.
+// A step is then about 5 us of latency with 8 CTAs and 3 us with one, against 21 us as three launches.
+// Exact in the same places as the products above (X in fp32 where those keep two fp16 planes).
+
+// Registers to 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+struct NsSmall {
+  const void* R;
+  const float* M;
+  int rows, cols;  // as the caller has them; m, n: the smaller and the larger
+  int m, n;
+  float mu, gs;
+  int nesterov;
+  const double* partials;  // of the momentum's squared norm
+  int count;
+  int steps;
+  int chunks;              // 64-column chunks of X a CTA keeps, at most 4
+  __nv_bfloat16* U;        // or
+  float* W;                // W <- keep W - rate X
+  float keep, rate;
+  uint32_t* status;
+};
+
+constexpr int kNsSmallThreads = 256;
+constexpr int kNsSmallRows = 128;
+constexpr int kNsSmallMaxChunks = 4;
+constexpr int kNsTile = kNsSmallRows * 128;  // bytes of a 128 x 64 fp16 tile
+constexpr int kNsSmallSmem = 1024 + (kNsSmallMaxChunks + 4) * kNsTile + kNsSmallRows * kNsSmallRows * 4;
+
+// 16-byte unit `unit` (of 8) of row r in a 128-byte-swizzled tile.
+__device__ __forceinline__ uint32_t ns_unit_offset(int r, int unit) {
+  return static_cast<uint32_t>(r * 128 + ((unit ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ uint4 pack_half8(const float* v) {
+  uint4 q;
+  __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+  return q;
+}
+
+template <typename T, bool MUON>
+__global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __grid_constant__ NsSmall p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  __shared__ float diag[kNsSmallRows];
+  __shared__ double norm_part[kNsSmallThreads / 32];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const hi = smem;                                   // X: [chunk][128][64]
+  uint8_t* const sA = hi + kNsSmallMaxChunks * kNsTile;       // A, and B below: [2][128][64]
+  uint8_t* const sB = sA + 2 * kNsTile;
+  float* const recv = reinterpret_cast<float*>(sB + 2 * kNsTile);  // [CTA][owned row][128] parts of A
+
+  const int tid = threadIdx.x, warp = tid / 32, half = warp / 4;
+  const uint32_t lane = lane_id();
+  const int r = 32 * (warp % 4) + static_cast<int>(lane);  // this thread's row (TMEM lane)
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const int owned = kNsSmallRows / static_cast<int>(ctas);  // rows of A a CTA adds up, a power of two
+  const int owned_bits = 31 - __clz(owned);
+  const int chunk0 = static_cast<int>(rank) * p.chunks;
+  const int chunks = max(0, min(p.chunks, (p.n + 63) / 64 - chunk0));
+
+  if (tid == 0) {
+    mbar_init(smem_addr(&done), 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_addr(&tmem_slot), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm_x = tmem_slot + (static_cast<uint32_t>(32 * (warp % 4)) << 16);  // X, 256 columns
+  const uint32_t tm_acc = tm_x + 256;                                                // the product at hand
+  const uint32_t acc0 = tmem_slot + 256;
+  griddep_wait();
+
+  // 1 / (||u|| + eps), in the same order in every CTA.
+  double s = 0.0;
+  for (int k = tid; k < p.count; k += kNsSmallThreads) s += p.partials[k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) norm_part[warp] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int w = 0; w < kNsSmallThreads / 32; ++w) s += norm_part[w];
+  const double inv = 1.0 / (sqrt(s) + kNsEps);
+
+  const bool tall = p.rows > p.cols;
+  auto value = [&](long long at) {
+    const float x = static_cast<float>(static_cast<const T*>(p.R)[at]);
+    float u = x;
+    if constexpr (MUON) {
+      const float mo = p.M[at];
+      u = p.nesterov ? fmaf(p.mu, mo, p.gs * x) : mo;
+    }
+    return static_cast<float>(static_cast<double>(u) * inv);
+  };
+  auto put_hi = [&](int cc, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(hi + cc * kNsTile + ns_unit_offset(r, 4 * half + q)) = pack_half8(v + 8 * q);
+  };
+  for (int cc = 0; cc < chunks; ++cc) {
+    float v[32];
+    const int col = (chunk0 + cc) * 64 + 32 * half;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int c = col + j;
+      v[j] = r < p.m && c < p.n ? value(tall ? static_cast<long long>(c) * p.cols + r : static_cast<long long>(r) * p.cols + c)
+                                : 0.0f;
+    }
+    tmem_st32(tm_x + 64 * cc + 32 * half, v);
+    put_hi(cc, v);
+  }
+  tmem_st_wait();
+
+  uint32_t parity = 0;
+  // Ends a phase of shared-memory writes and TMEM accesses, lets thread 0 issue MMAs, waits for them.
+  // A wait that runs out is recorded and the steps go on: every barrier is still met by every thread.
+  auto multiply = [&](auto issue) {
+    fence_async_proxy();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      fence_async_proxy();
+      issue();
+      umma_commit(smem_addr(&done));
+    }
+    __syncwarp();
+    mbar_wait_bounded(smem_addr(&done), parity, &abort_word, p.status, 41u);
+    parity ^= 1u;
+    tc_fence_after();
+  };
+  constexpr uint32_t kSquare = umma_idesc_f16(128, 128, false, false);
+
+  for (int step = 0; step < p.steps; ++step) {
+    // A = X X^T over this CTA's columns.
+    multiply([&] {
+      for (int cc = 0; cc < chunks; ++cc)
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t x = umma_desc_sw128(smem_addr(hi) + cc * kNsTile + ks * 32, 16, 1024);
+          umma_bf16(acc0, x, x, kSquare, (cc > 0 || ks > 0) ? 1u : 0u);
+        }
+    });
+    if (ctas == 1) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        float v[32];
+        tmem_ld32(tm_acc + 64 * half + 32 * part, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(sA + half * kNsTile + ns_unit_offset(r, 4 * part + q)) = pack_half8(v + 8 * q);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (64 * half + 32 * part + e == r) diag[r] = v[e];
+      }
+    } else {
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        float v[32];
+        tmem_ld32(tm_acc + 64 * half + 32 * part, v);
+        tmem_ld_wait();
+        const int c0 = 64 * half + 32 * part;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {  // row c0 + e of A, column r
+          const int owner = (c0 + e) >> owned_bits, row = (c0 + e) & (owned - 1);
+          st_cluster_f32(map_to_rank(smem_addr(recv + (static_cast<int>(rank) * owned + row) * kNsSmallRows + r), owner),
+                         chunks > 0 ? v[e] : 0.0f);
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();
+      for (int unit = tid; unit < owned * (kNsSmallRows / 8); unit += kNsSmallThreads) {
+        const int row = unit / (kNsSmallRows / 8), col = unit % (kNsSmallRows / 8) * 8;
+        float v[8] = {};
+        for (uint32_t c = 0; c < ctas; ++c) {
+          const float4* in = reinterpret_cast<const float4*>(recv + (static_cast<int>(c) * owned + row) * kNsSmallRows + col);
+          const float4 a = in[0], b = in[1];
+          v[0] += a.x;
+          v[1] += a.y;
+          v[2] += a.z;
+          v[3] += a.w;
+          v[4] += b.x;
+          v[5] += b.y;
+          v[6] += b.z;
+          v[7] += b.w;
+        }
+        const int R = static_cast<int>(rank) * owned + row;
+        const uint32_t at = smem_addr(sA) + (col / 64) * kNsTile + ns_unit_offset(R, (col % 64) / 8);
+        const uint4 q = pack_half8(v);
+        for (uint32_t c = 0; c < ctas; ++c) st_cluster_16(map_to_rank(at, c), q);
+        if (R >= col && R < col + 8) {
+          float d = v[0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) d = R == col + e ? v[e] : d;
+          for (uint32_t c = 0; c < ctas; ++c) st_cluster_f32(map_to_rank(smem_addr(diag + R), c), d);
+        }
+      }
+      fence_async_proxy();
+      __syncwarp();
+      cluster_sync_all();
+    }
+    // A^2, then B = b A + c A^2 - delta I.
+    multiply([&] {
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint64_t a = umma_desc_sw128(smem_addr(sA) + (ks / 4) * kNsTile + (ks % 4) * 32, 16, 1024);
+        umma_bf16(acc0, a, a, kSquare, ks > 0 ? 1u : 0u);
+      }
+    });
+    float tr = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kNsSmallRows / 32; ++k) tr += diag[32 * k + lane];  // rows past m are zero
+    tr = warp_sum(tr) / static_cast<float>(p.m);
+    const float delta = tr * fmaf(kNsC, tr, kNsB);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      float v[32];
+      tmem_ld32(tm_acc + 64 * half + 32 * part, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t at = half * kNsTile + ns_unit_offset(r, 4 * part + q);
+        const uint4 a4 = *reinterpret_cast<const uint4*>(sA + at);
+        const __half2* h = reinterpret_cast<const __half2*>(&a4);
+        float b[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = __half22float2(h[e]);
+          b[2 * e] = fmaf(kNsB, a.x, kNsC * v[8 * q + 2 * e]);
+          b[2 * e + 1] = fmaf(kNsB, a.y, kNsC * v[8 * q + 2 * e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (64 * half + 32 * part + 8 * q + e == r) b[e] -= delta;
+        *reinterpret_cast<uint4*>(sB + at) = pack_half8(b);
+      }
+    }
+    // X = (a + delta) X + B X.
+    const uint32_t wide = umma_idesc_f16(128, 64 * max(chunks, 1), false, true);
+    multiply([&] {
+      if (chunks > 0)
+        for (int ks = 0; ks < 8; ++ks)
+          umma_bf16(acc0, umma_desc_sw128(smem_addr(sB) + (ks / 4) * kNsTile + (ks % 4) * 32, 16, 1024),
+                    umma_desc_sw128(smem_addr(hi) + ks * 2048, kNsTile, 1024), wide, ks > 0 ? 1u : 0u);
+    });
+    const bool last = step + 1 == p.steps;
+    for (int cc = 0; cc < chunks; ++cc) {
+      float v[32], x[32];
+      __syncwarp();
+      tmem_ld32(tm_acc + 64 * cc + 32 * half, v);
+      tmem_ld32(tm_x + 64 * cc + 32 * half, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = fmaf(kNsA + delta, x[j], v[j]);
+      if (!last) {
+        tmem_st32(tm_x + 64 * cc + 32 * half, v);
+        put_hi(cc, v);
+        continue;
+      }
+      const int col = (chunk0 + cc) * 64 + 32 * half;
+      if (r >= p.m) continue;  // the next turn reconverges first
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const int c = col + j;
+        if (c >= p.n) continue;
+        const long long at = tall ? static_cast<long long>(c) * p.cols + r : static_cast<long long>(r) * p.cols + c;
+        if (!DP_DCHECK(in_buffer(at, 1, static_cast<long long>(p.rows) * p.cols), 61u, p.status)) continue;
+        if (p.U)
+          p.U[at] = __float2bfloat16_rn(v[j]);
+        else
+          p.W[at] = fmaf(p.keep, p.W[at], -p.rate * v[j]);
+      }
+    }
+    __syncwarp();
+    tmem_st_wait();
+  }
+  // Every MMA was waited for; after a wait that ran out one may still be at work.
+  __syncthreads();
+  griddep_launch_dependents();
+  if (tid == 0 && abort_word) {
+    umma_commit(smem_addr(&done));
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(smem_addr(&done), parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_slot, 512);
+  }
+}
+
 // ------------------------------------------------------------------------------ around them
 constexpr int kMuonThreads = 256;
 

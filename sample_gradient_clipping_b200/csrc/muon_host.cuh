@@ -104,6 +104,51 @@ struct MuonOut {
   float keep = 1.0f, rate = 0.0f;
 };
 
+// CTAs of the one-launch form, 0 where it does not serve: more than 128 rows (as m x n), or more
+// columns than 8 CTAs hold.  One CTA while its 256 columns suffice, since several exchange their
+// parts of A; then two chunks of 64 columns a CTA where there are CTAs enough.
+int ns_small_ctas(int m, int n) {
+  const int chunks = ceil_div(n, 64);
+  if (m > kNsSmallRows || chunks > 8 * kNsSmallMaxChunks) return 0;
+  if (chunks <= kNsSmallMaxChunks) return 1;
+  return chunks <= 4 * 2 ? 4 : 8;
+}
+
+template <typename T, bool MUON>
+dp_status ns_small(const T* R, const float* M, int rows, int cols, float mu, float gs, bool nesterov, int steps,
+                   const MuonOut& out, const double* partials, int count, int ctas, uint32_t* status,
+                   cudaStream_t stream) {
+  static std::atomic<bool> configured[64] = {};
+  int dev = 0;
+  DP_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+    DP_CUDA(cudaFuncSetAttribute(ns_small_kernel<T, MUON>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmallSmem));
+    if (dev >= 0 && dev < 64) configured[dev].store(true);
+  }
+  NsSmall p{};
+  p.R = R;
+  p.M = M;
+  p.rows = rows;
+  p.cols = cols;
+  p.m = std::min(rows, cols);
+  p.n = std::max(rows, cols);
+  p.mu = mu;
+  p.gs = gs;
+  p.nesterov = nesterov ? 1 : 0;
+  p.partials = partials;
+  p.count = count;
+  p.steps = steps;
+  p.chunks = ceil_div(ceil_div(p.n, 64), ctas);
+  p.U = out.U;
+  p.W = out.W;
+  p.keep = out.keep;
+  p.rate = out.rate;
+  p.status = status;
+  LaunchScope scope(kKindNsProduct, stream);
+  DP_LAUNCH_CLUSTER("ns_small_kernel", ctas, (ns_small_kernel<T, MUON>), ctas, kNsSmallThreads, kNsSmallSmem, stream, p);
+  return DP_OK;
+}
+
 template <typename T, bool MUON>
 dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs, bool nesterov, int steps,
                    const MuonOut& out, uint8_t* ws, cudaStream_t stream) {
@@ -122,6 +167,8 @@ dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs,
     DP_LAUNCH("muon_momentum_kernel", (muon_momentum_kernel<T, MUON>), blocks, kMuonThreads, 0, stream, R, M, vecs, mu, gs,
               nesterov ? 1 : 0, partials, status);
   }
+  if (const int ctas = ns_small_ctas(m, n))
+    return ns_small<T, MUON>(R, M, rows, cols, mu, gs, nesterov, steps, out, partials, blocks, ctas, status, stream);
   {
     LaunchScope scope(kKindMuonPrepare, stream);
     if (tall) {
