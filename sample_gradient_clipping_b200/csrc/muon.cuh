@@ -55,6 +55,7 @@ struct alignas(64) NsParams {
   __nv_bfloat16* U;
   float* W;
   float keep, rate;       // W <- keep W - rate X
+  int early;              // at most half the SMs are used
   uint32_t* status;
 };
 
@@ -77,8 +78,9 @@ struct NsConfig {
   static constexpr int STAGE_BYTES = 2 * OP_BYTES;
   static constexpr int STAGES = 6;
   static constexpr int NUM_BUFS = 2;
-  static constexpr int THREADS = 192;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;
+  static constexpr int THREADS = 320;                  // producer, MMA issuer, 8 epilogue warps
+  static constexpr int TURN_BYTES = KIND_ == kNsApply ? 8 * 32 * 33 * 4 : 0;  // a block an epilogue warp
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256 + TURN_BYTES;
   static constexpr uint32_t IDESC = umma_idesc_f16(PAIR ? 256 : 128, TILE, false, B_MN);
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per block");
 };
@@ -117,143 +119,187 @@ __device__ __forceinline__ float ns_delta(const float* __restrict__ trace, int o
   return t * fmaf(kNsC, t, kNsB);
 }
 
-// The 128 rows of a unit that this CTA holds: row0 + 32 wq + lane is this thread's.
-template <class Cfg>
-__device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsUnit& w, int row0, uint32_t tacc, int wq,
-                                            uint32_t lane, float delta) {
-  const int r = row0 + wq * 32 + static_cast<int>(lane);
-  const bool row_ok = r < p.m;
-  float tr = 0.0f;
-#pragma unroll 1
-  for (int c0 = 0; c0 < Cfg::TILE; c0 += 32) {
+// One epilogue warp's 32 x 32 block of kNsApply, turned through shared memory: X's planes and W are
+// read, and everything is written, in runs of 64 to 128 bytes along the rows.  The loads are issued
+// before the accumulator is waited for, and none stands behind a store (a row a lane, each load behind
+// the store before it, the last product of a 4096 x 11008 update took 434 us against 300 of the others).
+// r0, col: the block's first row and column; cols: its columns in the matrix (0 .. 32, a multiple of 8).
+__device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int col, int cols, uint32_t tacc,
+                                               float (*turn)[33], uint32_t lane, float factor) {
+  const int lr = static_cast<int>(lane) / 4, lc = static_cast<int>(lane) % 4 * 8;  // 8 rows of 4 x 8 columns
+  uint4 h[4], l[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = r0 + 8 * k + lr;
+    h[k] = l[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < p.m && lc < cols) {
+      const long long at = static_cast<long long>(row) * p.n + col + lc;
+      h[k] = *reinterpret_cast<const uint4*>(p.hi + at);
+      l[k] = *reinterpret_cast<const uint4*>(p.lo + at);
+    }
+  }
+  {
     float v[32];
     __syncwarp();
-    tmem_ld32(tacc + c0, v);
+    tmem_ld32(tacc, v);
     tmem_ld_wait();
-    const int col = w.nb * Cfg::TILE + c0;
-    const int cols = min(32, p.n - col);  // a multiple of 8
-    if (cols <= 0) continue;              // the same for the whole warp
-    if constexpr (Cfg::KIND == kNsApply) {
-      if (row_ok) {
-        const long long at = static_cast<long long>(r) * p.n + col;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (8 * q >= cols) break;
-          const uint4 h4 = *reinterpret_cast<const uint4*>(p.hi + at + 8 * q);
-          const uint4 l4 = *reinterpret_cast<const uint4*>(p.lo + at + 8 * q);
-          const __half2* h = reinterpret_cast<const __half2*>(&h4);
-          const __half2* l = reinterpret_cast<const __half2*>(&l4);
+    for (int e = 0; e < 32; ++e) turn[lane][e] = v[e];
+  }
+  __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = __half22float2(h[e]), b = __half22float2(l[e]);
-            v[8 * q + 2 * e] = fmaf(kNsA + delta, fmaf(b.x, 1.0f / kLoScale, a.x), v[8 * q + 2 * e]);
-            v[8 * q + 2 * e + 1] = fmaf(kNsA + delta, fmaf(b.y, 1.0f / kLoScale, a.y), v[8 * q + 2 * e + 1]);
-          }
-        }
-      }
-    } else if constexpr (Cfg::KIND == kNsPoly) {
-      if (row_ok) {
-        const long long at = static_cast<long long>(r) * p.n + col;
+  for (int k = 0; k < 4; ++k) {  // the new X, in place in the turned block
+    const __half2* a = reinterpret_cast<const __half2*>(&h[k]);
+    const __half2* b = reinterpret_cast<const __half2*>(&l[k]);
+    float x[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (8 * q >= cols) break;
-          const uint4 a4 = *reinterpret_cast<const uint4*>(p.A + at + 8 * q);
-          const __half2* h = reinterpret_cast<const __half2*>(&a4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = __half22float2(h[e]);
-            v[8 * q + 2 * e] = fmaf(kNsB, a.x, kNsC * v[8 * q + 2 * e]);
-            v[8 * q + 2 * e + 1] = fmaf(kNsB, a.y, kNsC * v[8 * q + 2 * e + 1]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (col + e == r) v[e] -= delta;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (col + e == r) tr = v[e];
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(a[e]), g = __half22float2(b[e]);
+      x[2 * e] = fmaf(factor, fmaf(g.x, 1.0f / kLoScale, f.x), turn[8 * k + lr][lc + 2 * e]);
+      x[2 * e + 1] = fmaf(factor, fmaf(g.y, 1.0f / kLoScale, f.y), turn[8 * k + lr][lc + 2 * e + 1]);
     }
-
-    const int mode = Cfg::KIND == kNsApply ? p.out_mode : kNsPlanes;
-    if (mode == kNsPlanes) {
-      if (row_ok) {
-        const long long at = static_cast<long long>(r) * p.n + col;
+    const int row = r0 + 8 * k + lr;
+    const bool in = row < p.m && lc < cols;
+    const long long at = static_cast<long long>(row) * p.n + col + lc;
+    if (p.out_mode == kNsPlanes) {
+      uint4 h4, l4;
+      __half2* nh = reinterpret_cast<__half2*>(&h4);
+      __half2* nl = reinterpret_cast<__half2*>(&l4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (8 * q >= cols || !DP_DCHECK(at + 8 * q + 8 <= static_cast<long long>(p.m) * p.n, 60u, p.status)) break;
-          uint4 h4, l4;
-          __half2* h = reinterpret_cast<__half2*>(&h4);
-          __half2* l = reinterpret_cast<__half2*>(&l4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[e] = __floats2half2_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-            if constexpr (Cfg::KIND == kNsApply) {
-              const float2 a = __half22float2(h[e]);
-              l[e] = __floats2half2_rn((v[8 * q + 2 * e] - a.x) * kLoScale, (v[8 * q + 2 * e + 1] - a.y) * kLoScale);
-            }
-          }
-          *reinterpret_cast<uint4*>(p.out + at + 8 * q) = h4;
-          if constexpr (Cfg::KIND == kNsApply) *reinterpret_cast<uint4*>(p.out_lo + at + 8 * q) = l4;
-        }
-        if constexpr (Cfg::SYMMETRIC) {  // the tile below the diagonal: column e of this one is its row
-          if (w.mb != w.nb) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e < cols) p.out[static_cast<long long>(col + e) * p.m + r] = __float2half_rn(v[e]);
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        nh[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+        const float2 f = __half22float2(nh[e]);
+        nl[e] = __floats2half2_rn((x[2 * e] - f.x) * kLoScale, (x[2 * e + 1] - f.y) * kLoScale);
       }
-    } else if (mode == kNsU) {
-      if (row_ok) {
-        __nv_bfloat16* dst = p.U + static_cast<long long>(r) * p.n + col;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (8 * q >= cols) break;
-          uint4 pk;
-          __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&pk);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-          *reinterpret_cast<uint4*>(dst + 8 * q) = pk;
-        }
+      if (in && DP_DCHECK(at + 8 <= static_cast<long long>(p.m) * p.n, 60u, p.status)) {
+        *reinterpret_cast<uint4*>(p.out + at) = h4;
+        *reinterpret_cast<uint4*>(p.out_lo + at) = l4;
       }
-    } else if (mode == kNsUT) {
-      if (row_ok) {
+    } else if (p.out_mode == kNsU) {
+      uint4 pk;
+      __nv_bfloat162* u = reinterpret_cast<__nv_bfloat162*>(&pk);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e < cols) p.U[static_cast<long long>(col + e) * p.m + r] = __float2bfloat16_rn(v[e]);
-      }
-    } else if (mode == kNsW) {
-      if (row_ok) {
-        float4* dst = reinterpret_cast<float4*>(p.W + static_cast<long long>(r) * p.n + col);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (4 * q >= cols) break;
-          float4 o = dst[q];
-          o.x = fmaf(p.keep, o.x, -p.rate * v[4 * q]);
-          o.y = fmaf(p.keep, o.y, -p.rate * v[4 * q + 1]);
-          o.z = fmaf(p.keep, o.z, -p.rate * v[4 * q + 2]);
-          o.w = fmaf(p.keep, o.w, -p.rate * v[4 * q + 3]);
-          dst[q] = o;
-        }
-      }
+      for (int e = 0; e < 4; ++e) u[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      if (in) *reinterpret_cast<uint4*>(p.U + at) = pk;
     } else {
-      if (row_ok) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (e < cols) {
-            float* dst = p.W + static_cast<long long>(col + e) * p.m + r;
-            *dst = fmaf(p.keep, *dst, -p.rate * v[e]);
-          }
-        }
+      for (int e = 0; e < 8; ++e) turn[8 * k + lr][lc + e] = x[e];
+    }
+  }
+  if (p.out_mode == kNsPlanes || p.out_mode == kNsU) return;
+  __syncwarp();
+  if (p.out_mode == kNsW) {  // 4 rows of 8 float4 at a time
+    float4 w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = r0 + 4 * k + static_cast<int>(lane) / 8, c = static_cast<int>(lane) % 8 * 4;
+      w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < p.m && c < cols) w[k] = *reinterpret_cast<const float4*>(p.W + static_cast<long long>(row) * p.n + col + c);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = 4 * k + static_cast<int>(lane) / 8, row = r0 + i, c = static_cast<int>(lane) % 8 * 4;
+      if (row < p.m && c < cols)
+        *reinterpret_cast<float4*>(p.W + static_cast<long long>(row) * p.n + col + c) =
+            make_float4(fmaf(p.keep, w[k].x, -p.rate * turn[i][c]), fmaf(p.keep, w[k].y, -p.rate * turn[i][c + 1]),
+                        fmaf(p.keep, w[k].z, -p.rate * turn[i][c + 2]), fmaf(p.keep, w[k].w, -p.rate * turn[i][c + 3]));
+    }
+    return;
+  }
+  // The caller's matrix is the transposed one: this block's columns are its rows, 32 of this block's
+  // rows a run.
+  const int row = r0 + static_cast<int>(lane);
+  if (p.out_mode == kNsUT) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (row < p.m && e < cols) p.U[static_cast<long long>(col + e) * p.m + row] = __float2bfloat16_rn(turn[lane][e]);
+    return;
+  }
+  float w[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) w[e] = row < p.m && e < cols ? p.W[static_cast<long long>(col + e) * p.m + row] : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (row < p.m && e < cols) p.W[static_cast<long long>(col + e) * p.m + row] = fmaf(p.keep, w[e], -p.rate * turn[lane][e]);
+}
+
+// One epilogue warp's 32 x 32 block of A or B: rows r0 .. (this thread's is r0 + lane), columns col ...
+template <class Cfg>
+__device__ __forceinline__ void ns_symmetric_block(const NsParams& p, const NsUnit& w, int r0, int col, int cols,
+                                                   uint32_t tacc, uint32_t lane, float delta, float& tr) {
+  const int r = r0 + static_cast<int>(lane);
+  const bool row_ok = r < p.m;
+  const long long at = static_cast<long long>(r) * p.n + col;
+  float v[32];
+  [[maybe_unused]] uint4 a4[4];
+  if constexpr (Cfg::KIND == kNsPoly) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      a4[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (row_ok && 8 * q < cols) a4[q] = *reinterpret_cast<const uint4*>(p.A + at + 8 * q);
+    }
+  }
+  __syncwarp();
+  tmem_ld32(tacc, v);
+  tmem_ld_wait();
+  if constexpr (Cfg::KIND == kNsPoly) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __half2* h = reinterpret_cast<const __half2*>(&a4[q]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = __half22float2(h[e]);
+        v[8 * q + 2 * e] = fmaf(kNsB, a.x, kNsC * v[8 * q + 2 * e]);
+        v[8 * q + 2 * e + 1] = fmaf(kNsB, a.y, kNsC * v[8 * q + 2 * e + 1]);
       }
     }
   }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    if (col + e != r) continue;
+    if constexpr (Cfg::KIND == kNsPoly)
+      v[e] -= delta;
+    else
+      tr = v[e];
+  }
+  if (!row_ok) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (8 * q >= cols || !DP_DCHECK(at + 8 * q + 8 <= static_cast<long long>(p.m) * p.n, 62u, p.status)) break;
+    uint4 h4;
+    __half2* h = reinterpret_cast<__half2*>(&h4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+    *reinterpret_cast<uint4*>(p.out + at + 8 * q) = h4;
+  }
+  if (w.mb == w.nb) return;
+  // The tile below the diagonal: column e of this one is its row, the warp's 32 rows a run of 64 bytes.
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (e < cols) p.out[static_cast<long long>(col + e) * p.m + r] = __float2half_rn(v[e]);
+}
+
+// This epilogue warp's share of a unit: 32 rows from r0, half the tile's columns.
+template <class Cfg>
+__device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsUnit& w, int r0, uint32_t tacc, int half,
+                                            float (*turn)[33], uint32_t lane, float delta) {
+  float tr = 0.0f;
+#pragma unroll 1
+  for (int c0 = half * (Cfg::TILE / 2); c0 < (half + 1) * (Cfg::TILE / 2); c0 += 32) {
+    const int col = w.nb * Cfg::TILE + c0;
+    const int cols = min(32, p.n - col);  // a multiple of 8
+    if (cols <= 0) break;
+    if constexpr (Cfg::KIND == kNsApply)
+      ns_apply_block(p, r0, col, cols, tacc + c0, turn, lane, kNsA + delta);
+    else
+      ns_symmetric_block<Cfg>(p, w, r0, col, cols, tacc + c0, lane, delta, tr);
+    __syncwarp();
+  }
   if constexpr (Cfg::KIND == kNsGram) {
-    if (w.mb == w.nb) {  // rows past m were zero-filled and add nothing
+    // The diagonal of these 32 rows lies in one half; rows past m were zero-filled and add nothing.
+    if (w.mb == w.nb && (r0 - w.nb * Cfg::TILE) / (Cfg::TILE / 2) == half) {
       tr = warp_sum(tr);
-      if (lane == 0 && row0 + wq * 32 < p.m) p.trace[(row0 + wq * 32) / 32] = tr;
+      if (lane == 0 && r0 < p.m) p.trace[r0 / 32] = tr;
     }
   }
 }
@@ -287,7 +333,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
     }
     for (int b = 0; b < Cfg::NUM_BUFS; ++b) {
       mbar_init(smem_addr(acc_full + b), 1);
-      mbar_init(smem_addr(acc_empty + b), 4 * kCtas);  // one arrival per epilogue warp of the tile
+      mbar_init(smem_addr(acc_empty + b), 8 * kCtas);  // one arrival per epilogue warp of the tile
     }
     mbar_init(smem_addr(drain), 1);
     *abort_flag = 0;
@@ -310,6 +356,8 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();  // barriers and TMEM are ready; global memory only from here
+  // A launch that leaves SMs free lets the next one set up there meanwhile.
+  if (p.early) griddep_launch_dependents();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (every CTA)
@@ -420,8 +468,10 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue warps 2..5 (every CTA)
-    const int wq = warp & 3;
+    // ------------------------------------------------------------ epilogue warps 2..9 (every CTA)
+    const int wq = warp & 3;           // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;  // and its half of the columns
+    float(*const turn)[33] = reinterpret_cast<float(*)[33]>(smem + Cfg::STAGES * Cfg::STAGE_BYTES + 256) + 32 * (warp - 2);
     const float delta = Cfg::KIND == kNsGram ? 0.0f : ns_delta(p.trace, p.order, lane);
     int buf = 0;
     uint32_t buf_phase = 0;
@@ -430,7 +480,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
       if (!mbar_wait_bounded(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 24u)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + buf * 256 + (static_cast<uint32_t>(wq * 32) << 16);
-      ns_epilogue<Cfg>(p, w, w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM, tacc, wq, lane, delta);
+      ns_epilogue<Cfg>(p, w, w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM + wq * 32, tacc, half, turn, lane, delta);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -472,9 +522,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 // r = 128, in one cluster.  Every CTA keeps up to 256 columns of X: in fp32 in TMEM, and their fp16
 // part as a shared-memory tile that serves both products (K-major for X X^T, MN-major for B X).  A step:
 //   each CTA forms X X^T of its columns; the CTAs add their parts (each the rows it owns, sent as
-//   columns: the matrix is symmetric, and so a warp's 32 lanes write 128 contiguous bytes) and send the
-//   rounded rows of A to all; each forms B, and then its columns of the next X.
-// A step is then about 5 us of latency with 8 CTAs and 3 us with one, against 21 us as three launches.
+//   columns: the matrix is symmetric, and so a warp's 32 lanes write 128 contiguous bytes; read by the
+//   owner instead, a step took 12 us) and send the rounded rows of A to all; each forms B, and then its
+//   columns of the next X.
+// A step is then about 8 us of latency with several CTAs (half of it the exchange) and 4 us with one,
+// against 18 us as three launches: 1024 x 128, five steps, 52 us against 105.
 // Exact in the same places as the products above (X in fp32 where those keep two fp16 planes).
 
 // Registers to 32 columns of this thread's TMEM lane.
@@ -525,6 +577,7 @@ struct NsSmall {
 constexpr int kNsSmallThreads = 256;
 constexpr int kNsSmallRows = 128;
 constexpr int kNsSmallMaxChunks = 4;
+constexpr int kNsSmallCtas = 16;      // at most (more than 8 where the device takes such clusters)
 constexpr int kNsTile = kNsSmallRows * 128;  // bytes of a 128 x 64 fp16 tile
 constexpr int kNsSmallSmem = 1024 + (kNsSmallMaxChunks + 4) * kNsTile + kNsSmallRows * kNsSmallRows * 4;
 
@@ -593,28 +646,51 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
   const double inv = 1.0 / (sqrt(s) + kNsEps);
 
   const bool tall = p.rows > p.cols;
-  auto value = [&](long long at) {
-    const float x = static_cast<float>(static_cast<const T*>(p.R)[at]);
-    float u = x;
-    if constexpr (MUON) {
-      const float mo = p.M[at];
-      u = p.nesterov ? fmaf(p.mu, mo, p.gs * x) : mo;
+  // X at 32 places: all loads first (a place outside the matrix reads element 0), then the arithmetic.
+  auto values = [&](auto place, float (&v)[32]) {
+    float x[32];
+    [[maybe_unused]] float mo[MUON ? 32 : 1];
+    bool in[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const long long at = place(j);
+      in[j] = at >= 0;
+      x[j] = static_cast<float>(static_cast<const T*>(p.R)[in[j] ? at : 0]);
+      if constexpr (MUON) mo[j] = p.M[in[j] ? at : 0];
     }
-    return static_cast<float>(static_cast<double>(u) * inv);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      float u = x[j];
+      if constexpr (MUON) u = p.nesterov ? fmaf(p.mu, mo[j], p.gs * x[j]) : mo[j];
+      v[j] = in[j] ? static_cast<float>(static_cast<double>(u) * inv) : 0.0f;
+    }
+  };
+  // Element (row, c) of the m x n matrix in the caller's, -1 outside.
+  auto place_of = [&](int row, int c) -> long long {
+    if (row >= p.m || c >= p.n) return -1;
+    return tall ? static_cast<long long>(c) * p.cols + row : static_cast<long long>(row) * p.cols + c;
   };
   auto put_hi = [&](int cc, const float (&v)[32]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       *reinterpret_cast<uint4*>(hi + cc * kNsTile + ns_unit_offset(r, 4 * half + q)) = pack_half8(v + 8 * q);
   };
+  // A wide matrix is read and written by rows: a warp's 32 x 32 block is turned in shared memory (the
+  // tiles of A and B, which hold nothing then).  A tall one already lies as the lanes hold it.
+  float(*const turn)[33] = reinterpret_cast<float(*)[33]>(sA) + 32 * warp;
   for (int cc = 0; cc < chunks; ++cc) {
     float v[32];
     const int col = (chunk0 + cc) * 64 + 32 * half;
+    if (tall) {
+      values([&](int j) { return place_of(r, col + j); }, v);
+    } else {
+      values([&](int j) { return place_of(32 * (warp % 4) + j, col + static_cast<int>(lane)); }, v);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int c = col + j;
-      v[j] = r < p.m && c < p.n ? value(tall ? static_cast<long long>(c) * p.cols + r : static_cast<long long>(r) * p.cols + c)
-                                : 0.0f;
+      for (int j = 0; j < 32; ++j) turn[j][lane] = v[j];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = turn[lane][j];
+      __syncwarp();
     }
     tmem_st32(tm_x + 64 * cc + 32 * half, v);
     put_hi(cc, v);
@@ -767,17 +843,35 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
         continue;
       }
       const int col = (chunk0 + cc) * 64 + 32 * half;
-      if (r >= p.m) continue;  // the next turn reconverges first
+      auto write = [&](auto place) {
+        float w[32];
+        if (!p.U) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int c = col + j;
-        if (c >= p.n) continue;
-        const long long at = tall ? static_cast<long long>(c) * p.cols + r : static_cast<long long>(r) * p.cols + c;
-        if (!DP_DCHECK(in_buffer(at, 1, static_cast<long long>(p.rows) * p.cols), 61u, p.status)) continue;
-        if (p.U)
-          p.U[at] = __float2bfloat16_rn(v[j]);
-        else
-          p.W[at] = fmaf(p.keep, p.W[at], -p.rate * v[j]);
+          for (int j = 0; j < 32; ++j) {
+            const long long at = place(j);
+            w[j] = p.W[at >= 0 ? at : 0];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const long long at = place(j);
+          if (at < 0 || !DP_DCHECK(in_buffer(at, 1, static_cast<long long>(p.rows) * p.cols), 61u, p.status)) continue;
+          if (p.U)
+            p.U[at] = __float2bfloat16_rn(v[j]);
+          else
+            p.W[at] = fmaf(p.keep, w[j], -p.rate * v[j]);
+        }
+      };
+      if (tall) {
+        write([&](int j) { return place_of(r, col + j); });
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) turn[lane][j] = v[j];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = turn[j][lane];
+        __syncwarp();
+        write([&](int j) { return place_of(32 * (warp % 4) + j, col + static_cast<int>(lane)); });
       }
     }
     __syncwarp();

@@ -58,7 +58,7 @@ dp_status map_f16(CUtensorMap* map, const __half* base, int rows, int cols, uint
 }
 
 template <class Cfg>
-dp_status launch_ns(const NsParams& p, cudaStream_t stream) {
+dp_status launch_ns(NsParams p, cudaStream_t stream) {
   auto kernel = [] {
     if constexpr (Cfg::PAIR)
       return ns_pair_kernel<Cfg>;
@@ -74,6 +74,7 @@ dp_status launch_ns(const NsParams& p, cudaStream_t stream) {
   }
   const int ctas = Cfg::PAIR ? 2 : 1;
   const int grid = std::min(p.num_units, sm_count() / ctas) * ctas;
+  p.early = 2 * grid <= sm_count() ? 1 : 0;
   LaunchScope scope(kKindNsProduct, stream);
   DP_LAUNCH("ns_kernel", kernel, grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
   return DP_OK;
@@ -104,27 +105,54 @@ struct MuonOut {
   float keep = 1.0f, rate = 0.0f;
 };
 
+template <typename T, bool MUON>
+dp_status ns_small_configure(bool* wide) {
+  static std::atomic<int> state[64] = {};  // 1: configured, 2: and clusters of 16 fit
+  int dev = 0;
+  DP_CUDA(cudaGetDevice(&dev));
+  int known = dev >= 0 && dev < 64 ? state[dev].load() : 0;
+  if (known == 0) {
+    auto kernel = ns_small_kernel<T, MUON>;
+    DP_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmallSmem));
+    known = 1;
+    // A cluster of more than 8 CTAs needs the device's consent and enough SMs in one group of them.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kNsSmallCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = kNsSmallCtas;
+    cfg.blockDim = kNsSmallThreads;
+    cfg.dynamicSmemBytes = kNsSmallSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0)
+      known = 2;
+    (void)cudaGetLastError();  // a refusal is an answer here, not an error of the call
+    if (dev >= 0 && dev < 64) state[dev].store(known);
+  }
+  *wide = known == 2;
+  return DP_OK;
+}
+
 // CTAs of the one-launch form, 0 where it does not serve: more than 128 rows (as m x n), or more
-// columns than 8 CTAs hold.  One CTA while its 256 columns suffice, since several exchange their
+// columns than its CTAs hold.  One CTA while its 256 columns suffice, since several exchange their
 // parts of A; then two chunks of 64 columns a CTA where there are CTAs enough.
-int ns_small_ctas(int m, int n) {
+int ns_small_ctas(int m, int n, bool wide) {
   const int chunks = ceil_div(n, 64);
-  if (m > kNsSmallRows || chunks > 8 * kNsSmallMaxChunks) return 0;
+  if (m > kNsSmallRows) return 0;
   if (chunks <= kNsSmallMaxChunks) return 1;
-  return chunks <= 4 * 2 ? 4 : 8;
+  if (chunks <= 4 * 2) return 4;
+  if (chunks <= 8 * kNsSmallMaxChunks) return 8;
+  return wide && chunks <= kNsSmallCtas * kNsSmallMaxChunks ? kNsSmallCtas : 0;
 }
 
 template <typename T, bool MUON>
 dp_status ns_small(const T* R, const float* M, int rows, int cols, float mu, float gs, bool nesterov, int steps,
                    const MuonOut& out, const double* partials, int count, int ctas, uint32_t* status,
                    cudaStream_t stream) {
-  static std::atomic<bool> configured[64] = {};
-  int dev = 0;
-  DP_CUDA(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    DP_CUDA(cudaFuncSetAttribute(ns_small_kernel<T, MUON>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmallSmem));
-    if (dev >= 0 && dev < 64) configured[dev].store(true);
-  }
   NsSmall p{};
   p.R = R;
   p.M = M;
@@ -155,6 +183,7 @@ dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs,
   const MuonLayout L = muon_layout(rows, cols);
   const bool tall = rows > cols;
   const int m = tall ? cols : rows, n = tall ? rows : cols;
+  dp_status st;
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   double* partials = reinterpret_cast<double*>(ws + L.partials);
   auto plane = [&](size_t o) { return reinterpret_cast<__half*>(ws + o); };
@@ -167,7 +196,9 @@ dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs,
     DP_LAUNCH("muon_momentum_kernel", (muon_momentum_kernel<T, MUON>), blocks, kMuonThreads, 0, stream, R, M, vecs, mu, gs,
               nesterov ? 1 : 0, partials, status);
   }
-  if (const int ctas = ns_small_ctas(m, n))
+  bool wide = false;
+  if (m <= kNsSmallRows && (st = ns_small_configure<T, MUON>(&wide)) != DP_OK) return st;
+  if (const int ctas = ns_small_ctas(m, n, wide))
     return ns_small<T, MUON>(R, M, rows, cols, mu, gs, nesterov, steps, out, partials, blocks, ctas, status, stream);
   {
     LaunchScope scope(kKindMuonPrepare, stream);
@@ -183,7 +214,6 @@ dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs,
                 plane(L.lo[0]));
     }
   }
-  dp_status st;
   CUtensorMap xk[2], xn[2], ak, bk;
   for (int k = 0; k < 2; ++k) {
     if ((st = map_f16(&xk[k], plane(L.hi[k]), m, n, 128)) != DP_OK) return st;

@@ -62,7 +62,7 @@ def _matrix(m, n, kind, seed):
 
 
 SHAPES = [(8, 8), (8, 200), (200, 8), (64, 32), (128, 128), (136, 120), (264, 264), (128, 1024), (1024, 128),
-          (16, 256), (40, 264), (128, 512), (72, 520), (2048, 120), (104, 2056), (128, 1416), (88, 1992),
+          (16, 256), (40, 264), (128, 512), (72, 520), (2048, 120), (104, 2056), (4096, 128), (24, 4104), (128, 1416), (88, 1992),
           (520, 1400), (1400, 520), (1096, 1096)]
 
 
