@@ -440,47 +440,45 @@ def dp_projected_adam_step(W, R, m, v, P, lr, t, beta1=0.9, beta2=0.999, eps=1e-
 
 # ---------------------------------------------------------------- embedding, RMS norm, Muon
 class _Launch:
-    """The stream one call is enqueued on.  Every tensor must be contiguous and on one CUDA
-    device; while the object is entered, that device and the call's stream are current, so that
-    what the binding allocates for the call belongs to that stream.  Entering gives the stream's
-    handle."""
+    """The stream one call is enqueued on.  Every tensor given (the first is not None) must be
+    contiguous and on one CUDA device; while the object is entered, that device and the call's
+    stream are current, so that what the binding allocates for the call belongs to that stream.
+    Entering gives the stream's handle.  ``names``: the tensors' names, for the errors."""
 
     __slots__ = ("index", "ctx")
 
-    def __init__(self, stream, **tensors):
+    def __init__(self, stream, names, *tensors):
         import torch
 
-        dev = None
-        for name, t in tensors.items():
+        index = self.index = tensors[0].get_device()
+        for name, t in zip(names.split(), tensors):
             if t is None:
                 continue
-            if not t.is_cuda:
+            at = t.get_device()
+            if at < 0:
                 raise ValueError(f"{name} must be a CUDA tensor")
+            if at != index:
+                raise ValueError(f"{name} is on {t.device}, the first tensor on {tensors[0].device}")
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, the first tensor on {dev}")
-        self.index = dev.index
-        self.ctx = ()
+        self.ctx = None
         if stream is not None:   # also makes the stream's device current
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            self.ctx = (torch.cuda.stream(stream),)
-        elif dev.index != torch.cuda.current_device():
-            self.ctx = (torch.cuda.device(dev),)
+                stream = torch.cuda.ExternalStream(stream, device=tensors[0].device)
+            if stream.device != tensors[0].device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {tensors[0].device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(index)
 
     def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
         return _raw_stream(self.index)
 
     def __exit__(self, *exc):
-        for c in self.ctx:
-            c.__exit__(*exc)
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
         return False
 
 
@@ -494,7 +492,7 @@ def _raw_stream(index):
 
 
 def _expect(t, name, shape, dtype):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
@@ -530,7 +528,7 @@ def dp_embedding_lookup(W, ids, scale=1.0, out=None, out_dtype=None, stream=None
     dtype = out.dtype if out is not None else (out_dtype or W.dtype)
     shape = (*ids.shape, d)
     _expect(out, "out", shape, dtype)
-    with _Launch(stream, W=W, ids=ids, out=out) as s:
+    with _Launch(stream, "W ids out", W, ids, out) as s:
         Y = torch.empty(shape, dtype=dtype, device=W.device) if out is None else out
         if ids.numel():
             check(lib().dp_embedding_lookup(_ptr(W), _dtype_code(W), _ptr(ids), _index_code(ids), float(scale),
@@ -559,7 +557,7 @@ def dp_embedding_per_sample_norms(ids, dY, V, scale=1.0, padding_idx=None, norms
 
     B, T, d = _embedding_dims(ids, dY)
     _expect(norms, "norms", (B,), torch.float32)
-    with _Launch(stream, dY=dY, ids=ids, norms=norms, workspace=workspace) as s:
+    with _Launch(stream, "dY ids norms workspace", dY, ids, norms, workspace) as s:
         ws = _scratch(workspace, embedding_workspace_size(B, T, int(V), d, _dtype_code(dY)), dY.device,
                       "dp_embedding_workspace_size")
         if norms is None:
@@ -581,7 +579,7 @@ def dp_embedding_clip_accumulate(ids, dY, norms, C, G_sum, scale=1.0, padding_id
     V = int(G_sum.shape[0])
     _expect(G_sum, "G_sum", (V, d), torch.float32)
     _expect(norms, "norms", (B,), torch.float32)
-    with _Launch(stream, dY=dY, ids=ids, norms=norms, G_sum=G_sum, workspace=workspace) as s:
+    with _Launch(stream, "dY ids norms G_sum workspace", dY, ids, norms, G_sum, workspace) as s:
         ws = _scratch(workspace, embedding_workspace_size(B, T, V, d, _dtype_code(dY)), dY.device,
                       "dp_embedding_workspace_size")
         check(lib().dp_embedding_clip_accumulate(_ptr(ids), _index_code(ids), _ptr(dY), _dtype_code(dY), B, T, V, d,
@@ -604,7 +602,7 @@ def dp_embedding_step(ids, dY, V, C, sigma, seed, step, layer_id, scale=1.0, pad
     _expect(G_out, "G_out", (V, d), torch.float32)
     _expect(norms_out, "norms_out", (B,), torch.float32)
     dstep = _device_step(step)
-    with _Launch(stream, dY=dY, ids=ids, norms_out=norms_out, G_out=G_out, workspace=workspace, step=dstep) as s:
+    with _Launch(stream, "dY ids norms_out G_out workspace step", dY, ids, norms_out, G_out, workspace, dstep) as s:
         ws = _scratch(workspace, embedding_workspace_size(B, T, V, d, _dtype_code(dY)), dY.device,
                       "dp_embedding_workspace_size")
         if G_out is None:
@@ -631,7 +629,7 @@ def dp_rmsnorm(X, gain, eps=1e-6, residual=None, H_out=None, Y=None, stream=None
     _expect(Y, "Y", X.shape, X.dtype)
     if residual is None and H_out is not None:
         raise ValueError("H_out needs a residual: without one h is X itself")
-    with _Launch(stream, X=X, gain=gain, residual=residual, H_out=H_out, Y=Y) as s:
+    with _Launch(stream, "X gain residual H_out Y", X, gain, residual, H_out, Y) as s:
         Y = torch.empty_like(X) if Y is None else Y
         H = X
         if residual is not None:
@@ -667,8 +665,8 @@ def dp_rmsnorm_backward(H, gain, dY, eps=1e-6, residual_grad=None, dX=None, per_
     B, T, d = _norm_dims(H, dY, gain, residual_grad, dX)
     _expect(per_sample, "per_sample", (B, d), torch.float32)
     _expect(norms, "norms", (B,), torch.float32)
-    with _Launch(stream, H=H, gain=gain, dY=dY, residual_grad=residual_grad, dX=dX, per_sample=per_sample,
-                 norms=norms, workspace=workspace) as s:
+    with _Launch(stream, "H gain dY residual_grad dX per_sample norms workspace", H, gain, dY, residual_grad, dX,
+                 per_sample, norms, workspace) as s:
         ws = _scratch(workspace, rmsnorm_workspace_size(B, T, d, _dtype_code(H)), H.device,
                       "dp_rmsnorm_workspace_size")
         dX = torch.empty_like(H) if dX is None else dX
@@ -692,7 +690,7 @@ def dp_rmsnorm_clip_accumulate(per_sample, norms, C, G_sum, stream=None):
     _expect(per_sample, "per_sample", (B, d), torch.float32)
     _expect(norms, "norms", (B,), torch.float32)
     _expect(G_sum, "G_sum", (d,), torch.float32)
-    with _Launch(stream, per_sample=per_sample, norms=norms, G_sum=G_sum) as s:
+    with _Launch(stream, "per_sample norms G_sum", per_sample, norms, G_sum) as s:
         check(lib().dp_rmsnorm_clip_accumulate(_ptr(per_sample), _ptr(norms), B, d, float(C), _ptr(G_sum), s),
               "dp_rmsnorm_clip_accumulate")
     return G_sum
@@ -711,8 +709,8 @@ def dp_rmsnorm_step(H, gain, dY, C, sigma, seed, step, layer_id, eps=1e-6, resid
     _expect(G_out, "G_out", (d,), torch.float32)
     _expect(norms_out, "norms_out", (B,), torch.float32)
     dstep = _device_step(step)
-    with _Launch(stream, H=H, gain=gain, dY=dY, residual_grad=residual_grad, dX=dX, norms_out=norms_out, G_out=G_out,
-                 workspace=workspace, step=dstep) as s:
+    with _Launch(stream, "H gain dY residual_grad dX norms_out G_out workspace step", H, gain, dY, residual_grad, dX,
+                 norms_out, G_out, workspace, dstep) as s:
         ws = _scratch(workspace, rmsnorm_workspace_size(B, T, d, _dtype_code(H)), H.device,
                       "dp_rmsnorm_workspace_size")
         dX = torch.empty_like(H) if dX is None else dX
@@ -740,7 +738,7 @@ def dp_orthogonalize(G, steps=5, U=None, workspace=None, stream=None):
         raise ValueError("G must be [rows, cols]")
     rows, cols = int(G.shape[0]), int(G.shape[1])
     _expect(U, "U", (rows, cols), torch.bfloat16)
-    with _Launch(stream, G=G, U=U, workspace=workspace) as s:
+    with _Launch(stream, "G U workspace", G, U, workspace) as s:
         ws = _scratch(workspace, muon_workspace_size(rows, cols), G.device, "dp_muon_workspace_size")
         U = torch.empty(rows, cols, dtype=torch.bfloat16, device=G.device) if U is None else U
         check(lib().dp_orthogonalize(_ptr(G), _dtype_code(G), rows, cols, int(steps), _ptr(U), _ptr(ws),
@@ -759,7 +757,7 @@ def dp_muon_step(W, R, M, lr, momentum=0.95, nesterov=True, weight_decay=0.0, gr
     for name, t in (("W", W), ("R", R), ("M", M)):
         _expect(t, name, W.shape, torch.float32)
     d_in, d_out = int(W.shape[0]), int(W.shape[1])
-    with _Launch(stream, W=W, R=R, M=M, workspace=workspace) as s:
+    with _Launch(stream, "W R M workspace", W, R, M, workspace) as s:
         ws = _scratch(workspace, muon_workspace_size(d_in, d_out), W.device, "dp_muon_workspace_size")
         check(lib().dp_muon_step(_ptr(W), _ptr(R), _ptr(M), d_in, d_out, float(lr), float(momentum),
                                  1 if nesterov else 0, float(weight_decay), float(grad_scale), float(update_scale),
