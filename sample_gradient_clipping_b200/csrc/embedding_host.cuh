@@ -182,6 +182,9 @@ dp_status emb_check(const EmbCall& s, const void* ids, dp_index it, const void* 
   return DP_OK;
 }
 
+// Rows of at least this many elements are looked up a warp at a time.
+constexpr int kEmbWideRow = 512;
+
 template <typename TI, typename TO>
 dp_status emb_lookup_as(const void* W, const void* ids, dp_index it, float scale, long long N, int V, int d, void* Y,
                         cudaStream_t stream) {
@@ -190,6 +193,14 @@ dp_status emb_lookup_as(const void* W, const void* ids, dp_index it, float scale
   const long long vecs = N * (d / wide);
   const int grid = stream_grid(static_cast<unsigned long long>((vecs + 3) / 4), 256);
   LaunchScope scope(kKindEmbLookup, stream);
+  if (wide == 8 && d >= kEmbWideRow && d <= 65535 * 1024) {
+    const int segments = ceil_div(d, 1024);
+    const long long rows = std::max(1ll, std::min((N + 7) / 8, static_cast<long long>(sm_count()) * 32 / segments));
+    DP_LAUNCH("emb_lookup_wide_kernel", (emb_lookup_wide_kernel<TI, TO>),
+              dim3(static_cast<unsigned>(rows), static_cast<unsigned>(segments)), 256, 0, stream, static_cast<const TI*>(W),
+              ids, it == DP_I64 ? 1 : 0, scale, N, V, d, static_cast<TO*>(Y));
+    return DP_OK;
+  }
   if constexpr (sizeof(TI) == 4 && sizeof(TO) == 4) {
     if (wide == 4) {
       DP_LAUNCH("emb_lookup_kernel", (emb_lookup_kernel<TI, TO, 4>), grid, 256, 0, stream, static_cast<const TI*>(W), ids,
