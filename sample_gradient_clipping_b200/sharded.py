@@ -13,6 +13,9 @@ The all-reduce of linear l is issued as soon as its sum is enqueued, so it overl
 linear's kernels.  With flat (whole-block) clipping the clip factor of a sample needs only
 that sample's norms over the block's linears, which live on the same rank.
 
+A layer is a linear (X, dY), an embedding table (ids, dY, V) or the gain of an RMS norm (H, gain,
+dY), each with its own entry points of the library.
+
 ``ops`` supplies the per-rank compute.  The default is the CUDA library; there is no CPU
 path in the product.  Tests substitute their own ops to check this orchestration on CPU
 ranks with the gloo backend.
@@ -42,7 +45,20 @@ class LibraryOps:
         return self._ws
 
     def local_sum(self, layer, C, seed, step, stream=None):
-        """Clipped sum of this rank's samples for one linear (sigma = 0, so no noise)."""
+        """Clipped sum of this rank's samples for one layer (sigma = 0, so no noise)."""
+        if "ids" in layer:
+            G, n = self._lib.dp_embedding_step(layer["ids"], layer["dY"], layer["V"], C, 0.0, seed, step,
+                                               layer["layer_id"], norms_out=layer.get("norms_out"),
+                                               G_out=layer.get("G_out"), stream=stream, **self._embedding(layer))
+            layer["G_out"], layer["norms_out"] = G, n
+            return G
+        if "gain" in layer:
+            layer["dX"], G, n = self._lib.dp_rmsnorm_step(layer["H"], layer["gain"], layer["dY"], C, 0.0, seed, step,
+                                                          layer["layer_id"], dX=layer.get("dX"),
+                                                          norms_out=layer.get("norms_out"), G_out=layer.get("G_out"),
+                                                          stream=stream, **self._norm(layer))
+            layer["G_out"], layer["norms_out"] = G, n
+            return G
         G, n = self._lib.dp_linear_step(layer["X"], layer["dY"], C, 0.0, seed, step, layer["layer_id"],
                                         method=self.method, norms_out=layer.get("norms_out"),
                                         G_out=layer.get("G_out"), workspace=self._workspace(layer["X"], layer["dY"]),
@@ -52,11 +68,60 @@ class LibraryOps:
 
     def local_block_sums(self, layers, C, seed, step, stream=None):
         """Flat clipping over the block on this rank's samples, without noise."""
+        if any("ids" in layer or "gain" in layer for layer in layers):
+            return self._mixed_sums(layers, C, stream)
         outs, norms, flat = self._lib.dp_block_step(layers, mode="flat", C=C, sigma=0.0, seed=seed, step=step,
                                                     method=self.method, stream=stream)
         for layer, G, n in zip(layers, outs, norms):
             layer["G_out"], layer["norms_out"] = G, n
         return outs, flat
+
+    @staticmethod
+    def _embedding(layer):
+        return {"scale": layer.get("scale", 1.0), "padding_idx": layer.get("padding_idx")}
+
+    @staticmethod
+    def _norm(layer):
+        return {"eps": layer.get("eps", 1e-6), "residual_grad": layer.get("residual_grad")}
+
+    def _mixed_sums(self, layers, C, stream):
+        """Flat clipping over linears, tables and gains: every layer's norms first, then each
+        layer's sum with the factors of the combined norms."""
+        import contextlib
+
+        import torch
+
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            for layer in layers:
+                if "ids" in layer:
+                    n = self._lib.dp_embedding_per_sample_norms(layer["ids"], layer["dY"], layer["V"],
+                                                                norms=layer.get("norms_out"), **self._embedding(layer))
+                elif "gain" in layer:
+                    layer["dX"], layer["per_sample"], n = self._lib.dp_rmsnorm_backward(
+                        layer["H"], layer["gain"], layer["dY"], dX=layer.get("dX"), norms=layer.get("norms_out"),
+                        **self._norm(layer))
+                else:
+                    n = self._lib.dp_per_sample_norms(layer["X"], layer["dY"], method=self.method,
+                                                      norms=layer.get("norms_out"),
+                                                      workspace=self._workspace(layer["X"], layer["dY"]))
+                layer["norms_out"] = n
+            flat = torch.stack([layer["norms_out"] for layer in layers]).double().square().sum(0).sqrt().float()
+            for layer in layers:
+                G = layer.get("G_out")
+                if G is None:
+                    shape = ((layer["V"], layer["dY"].shape[2]) if "ids" in layer else
+                             layer["gain"].shape if "gain" in layer else (layer["X"].shape[2], layer["dY"].shape[2]))
+                    G = torch.empty(shape, dtype=torch.float32, device=layer["dY"].device)
+                G.zero_()
+                if "ids" in layer:
+                    self._lib.dp_embedding_clip_accumulate(layer["ids"], layer["dY"], flat, C, G, **self._embedding(layer))
+                elif "gain" in layer:
+                    self._lib.dp_rmsnorm_clip_accumulate(layer["per_sample"], flat, C, G)
+                else:
+                    self._lib.dp_clip_accumulate(layer["X"], layer["dY"], flat, C, G,
+                                                 workspace=self._workspace(layer["X"], layer["dY"]))
+                layer["G_out"] = G
+        return [layer["G_out"] for layer in layers], flat
 
     def add_noise(self, G, std, seed, step, layer_id, stream=None):
         self._lib.dp_add_noise(G, std, seed, step, layer_id, stream=stream)
@@ -66,7 +131,9 @@ def sharded_step(layers, sigma, seed, step, mode="per_layer", C=None, group=None
     """One privatised step of a block whose batch is split across the ranks of ``group``.
 
     ``layers``: this rank's shard, dicts with X [B_r, T, d_in], dY [B_r, T, d_out], layer_id, C
-    (per-layer bound) and optional G_out / norms_out.  ``mode``: "per_layer" (each linear its
+    (per-layer bound) and optional G_out / norms_out.  Instead of X: ids [B_r, T] and V (and scale,
+    padding_idx) for an embedding table; H [B_r, T, d] and gain [d] (and eps, residual_grad) for an
+    RMS norm, whose dX is then put into the dict.  ``mode``: "per_layer" (each linear its
     own C_l, noise sigma * C_l) or "flat" (bound ``C`` for the whole block, noise sigma * C).
     Every rank returns the same noisy global sums, one per linear, and its own samples' norms.
     """
