@@ -120,24 +120,29 @@ __device__ __forceinline__ float ns_delta(const float* __restrict__ trace, int o
 }
 
 // One epilogue warp's 32 x 32 block of kNsApply, turned through shared memory: X's planes and W are
-// read, and everything is written, in runs of 64 to 128 bytes along the rows.  The loads are issued
-// before the accumulator is waited for, and none stands behind a store (a row a lane, each load behind
-// the store before it, the last product of a 4096 x 11008 update took 434 us against 300 of the others).
+// read, and everything is written, in runs of 64 to 128 bytes along the rows.  The planes' loads are a
+// block ahead (the first before the accumulator is waited for), and no load stands behind a store (a row
+// a lane, each load behind the store before it, the last product of a 4096 x 11008 update took 434 us).
 // r0, col: the block's first row and column; cols: its columns in the matrix (0 .. 32, a multiple of 8).
-__device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int col, int cols, uint32_t tacc,
-                                               float (*turn)[33], uint32_t lane, float factor) {
-  const int lr = static_cast<int>(lane) / 4, lc = static_cast<int>(lane) % 4 * 8;  // 8 rows of 4 x 8 columns
-  uint4 h[4], l[4];
+struct NsPlanes {
+  uint4 h[4], l[4];  // row 8 k + lane / 4, columns 8 (lane % 4) ..
+};
+__device__ __forceinline__ void ns_load_planes(const NsParams& p, int r0, int col, uint32_t lane, NsPlanes& x) {
+  const int lr = static_cast<int>(lane) / 4, c = col + static_cast<int>(lane) % 4 * 8;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int row = r0 + 8 * k + lr;
-    h[k] = l[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < p.m && lc < cols) {
-      const long long at = static_cast<long long>(row) * p.n + col + lc;
-      h[k] = *reinterpret_cast<const uint4*>(p.hi + at);
-      l[k] = *reinterpret_cast<const uint4*>(p.lo + at);
+    x.h[k] = x.l[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < p.m && c < p.n) {
+      const long long at = static_cast<long long>(row) * p.n + c;
+      x.h[k] = *reinterpret_cast<const uint4*>(p.hi + at);
+      x.l[k] = *reinterpret_cast<const uint4*>(p.lo + at);
     }
   }
+}
+__device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int col, int cols, uint32_t tacc,
+                                               float (*turn)[33], uint32_t lane, float factor, const NsPlanes& old) {
+  const int lr = static_cast<int>(lane) / 4, lc = static_cast<int>(lane) % 4 * 8;  // 8 rows of 4 x 8 columns
   {
     float v[32];
     __syncwarp();
@@ -149,8 +154,8 @@ __device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int co
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {  // the new X, in place in the turned block
-    const __half2* a = reinterpret_cast<const __half2*>(&h[k]);
-    const __half2* b = reinterpret_cast<const __half2*>(&l[k]);
+    const __half2* a = reinterpret_cast<const __half2*>(&old.h[k]);
+    const __half2* b = reinterpret_cast<const __half2*>(&old.l[k]);
     float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -282,16 +287,20 @@ __device__ __forceinline__ void ns_symmetric_block(const NsParams& p, const NsUn
 // This epilogue warp's share of a unit: 32 rows from r0, half the tile's columns.
 template <class Cfg>
 __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsUnit& w, int r0, uint32_t tacc, int half,
-                                            float (*turn)[33], uint32_t lane, float delta) {
+                                            float (*turn)[33], uint32_t lane, float delta, const NsPlanes& first) {
   float tr = 0.0f;
+  [[maybe_unused]] NsPlanes ahead;
+  if constexpr (Cfg::KIND == kNsApply) ahead = first;
 #pragma unroll 1
   for (int c0 = half * (Cfg::TILE / 2); c0 < (half + 1) * (Cfg::TILE / 2); c0 += 32) {
     const int col = w.nb * Cfg::TILE + c0;
     const int cols = min(32, p.n - col);  // a multiple of 8
     if (cols <= 0) break;
-    if constexpr (Cfg::KIND == kNsApply)
-      ns_apply_block(p, r0, col, cols, tacc + c0, turn, lane, kNsA + delta);
-    else
+    if constexpr (Cfg::KIND == kNsApply) {
+      const NsPlanes old = ahead;
+      if (c0 + 32 < (half + 1) * (Cfg::TILE / 2)) ns_load_planes(p, r0, col + 32, lane, ahead);
+      ns_apply_block(p, r0, col, cols, tacc + c0, turn, lane, kNsA + delta, old);
+    } else
       ns_symmetric_block<Cfg>(p, w, r0, col, cols, tacc + c0, lane, delta, tr);
     __syncwarp();
   }
@@ -477,10 +486,13 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
     uint32_t buf_phase = 0;
     for (int u = first; u < p.num_units; u += step) {
       const NsUnit w = ns_unit<Cfg>(p, u);
+      const int r0 = w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM + wq * 32;
+      NsPlanes planes;
+      if constexpr (Cfg::KIND == kNsApply) ns_load_planes(p, r0, w.nb * Cfg::TILE + half * (Cfg::TILE / 2), lane, planes);
       if (!mbar_wait_bounded(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 24u)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + buf * 256 + (static_cast<uint32_t>(wq * 32) << 16);
-      ns_epilogue<Cfg>(p, w, w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM + wq * 32, tacc, half, turn, lane, delta);
+      ns_epilogue<Cfg>(p, w, r0, tacc, half, turn, lane, delta, planes);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {

@@ -7,7 +7,9 @@
 Ops: ``noise`` (dp_add_noise on an fp32 [rows, cols] buffer), ``projection``
 (dp_projection_matrix, bf16 [rows, cols]), ``philox`` (dp_philox_blocks, rows*cols/4 blocks),
 ``norms`` (dp_per_sample_norms) and ``clip_accumulate`` (dp_clip_accumulate) on seeded bf16
-inputs [B, T, d].  Prints one JSON line: microseconds per call (CUDA events around ``--iters``
+inputs [B, T, d], ``lookup`` and ``embedding`` (dp_embedding_lookup, dp_embedding_step with a table
+of ``rows`` rows of width ``d-in``, ids as frequent as 1 / rank), ``rmsnorm_step`` (dp_rmsnorm_step of
+[B, T, d-in] with a residual gradient) and ``muon`` (dp_muon_step of fp32 [rows, cols]).  Prints one JSON line: microseconds per call (CUDA events around ``--iters``
 calls after ``--warmup`` calls) and the algorithmic bytes or flops per second.
 """
 from __future__ import annotations
@@ -22,7 +24,8 @@ def main(argv=None):
     from . import _lib, inputs
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", required=True, choices=["noise", "projection", "philox", "norms", "clip_accumulate"])
+    ap.add_argument("--op", required=True, choices=["noise", "projection", "philox", "norms", "clip_accumulate",
+                                                   "lookup", "embedding", "rmsnorm_step", "muon"])
     ap.add_argument("--rows", type=int, default=8192)
     ap.add_argument("--cols", type=int, default=8192)
     ap.add_argument("--B", type=int, default=8)
@@ -30,6 +33,7 @@ def main(argv=None):
     ap.add_argument("--d-in", type=int, default=4096)
     ap.add_argument("--d-out", type=int, default=4096)
     ap.add_argument("--method", default="auto", choices=list(_lib.METHODS))
+    ap.add_argument("--sigma", type=float, default=1.0)
     ap.add_argument("--iters", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=3)
     a = ap.parse_args(argv)
@@ -49,6 +53,36 @@ def main(argv=None):
         out = torch.empty(nblk, 4, dtype=torch.int32, device=dev)
         call = lambda k: _lib.dp_philox_blocks(nblk, 7, k, 3, 0, out=out)
         work, unit = 16.0 * nblk, "GB/s"
+    elif a.op in ("lookup", "embedding"):
+        gen = torch.Generator(device=dev).manual_seed(1)
+        u = torch.rand(a.B, a.T, generator=gen, device=dev, dtype=torch.float64)
+        ids = (rows ** u).long().clamp(1, rows) - 1
+        tokens = a.B * a.T * a.d_in * 2.0
+        if a.op == "lookup":
+            W = torch.randn(rows, a.d_in, generator=gen, device=dev).to(torch.bfloat16)
+            Y = torch.empty(a.B, a.T, a.d_in, dtype=torch.bfloat16, device=dev)
+            call = lambda k: _lib.dp_embedding_lookup(W, ids, out=Y)
+            work = 2 * tokens
+        else:
+            dY = torch.randn(a.B, a.T, a.d_in, generator=gen, device=dev).to(torch.bfloat16)
+            G = torch.empty(rows, a.d_in, dtype=torch.float32, device=dev)
+            ws = torch.empty(_lib.embedding_workspace_size(a.B, a.T, rows, a.d_in), dtype=torch.uint8, device=dev)
+            call = lambda k: _lib.dp_embedding_step(ids, dY, rows, 1.0, a.sigma, 7, k, 3, G_out=G, workspace=ws)
+            work = tokens + 4.0 * rows * a.d_in
+        unit = "GB/s"
+    elif a.op == "rmsnorm_step":
+        H, dY, res = (torch.randn(a.B, a.T, a.d_in, device=dev).to(torch.bfloat16) for _ in range(3))
+        gain = torch.ones(a.d_in, device=dev)
+        ws = torch.empty(_lib.rmsnorm_workspace_size(a.B, a.T, a.d_in), dtype=torch.uint8, device=dev)
+        dX = torch.empty_like(H)
+        call = lambda k: _lib.dp_rmsnorm_step(H, gain, dY, 1.0, a.sigma, 7, k, 3, residual_grad=res, dX=dX, workspace=ws)
+        work, unit = 8.0 * a.B * a.T * a.d_in, "GB/s"
+    elif a.op == "muon":
+        W, R, M = (torch.randn(rows, cols, device=dev) for _ in range(3))
+        ws = torch.empty(_lib.muon_workspace_size(rows, cols), dtype=torch.uint8, device=dev)
+        call = lambda k: _lib.dp_muon_step(W, R, M, 1e-3, workspace=ws)
+        m, n = float(min(rows, cols)), float(max(rows, cols))
+        work, unit = 5 * (3 * m * m * n + m ** 3), "TFLOP/s"    # X X^T and A^2 are symmetric
     else:
         w = inputs.custom("kernel_bench", B=a.B, T=a.T, d_in=a.d_in, d_out=a.d_out, C=1.0, sigma=0.0, seed=1)
         d = inputs.generate(w)
@@ -76,7 +110,9 @@ def main(argv=None):
     us = e0.elapsed_time(e1) * 1e3 / a.iters
     rate = work / (us * 1e-6) / (1e9 if unit == "GB/s" else 1e12)
     print(json.dumps({"op": a.op, "us_per_call": us, "rate": rate, "unit": unit,
-                      "shape": {"rows": rows, "cols": cols} if a.op in ("noise", "projection", "philox")
+                      "shape": {"rows": rows, "cols": cols} if a.op in ("noise", "projection", "philox", "muon")
+                      else {"B": a.B, "T": a.T, "rows": rows, "d": a.d_in}
+                      if a.op in ("lookup", "embedding", "rmsnorm_step")
                       else {"B": a.B, "T": a.T, "d_in": a.d_in, "d_out": a.d_out, "method": a.method}}))
 
 
