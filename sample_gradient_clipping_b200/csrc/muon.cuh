@@ -59,14 +59,26 @@ struct alignas(64) NsParams {
   uint32_t* status;
 };
 
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4)                                 // D: f32; A and B format 0: f16
          | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <bool PAIR_, int KIND_>
+// SPLIT: the CTAs of a cluster share one 128 x 128 tile of a symmetric product, each a run of its K
+// blocks; each then adds up and stores the rows that it owns.  For products of few tiles and long K.
+template <bool PAIR_, int KIND_, bool SPLIT_ = false>
 struct NsConfig {
+  static constexpr bool SPLIT = SPLIT_;
   static constexpr bool PAIR = PAIR_;
   static constexpr int KIND = KIND_;
   static constexpr int BM = 128;                       // rows a CTA
@@ -76,13 +88,15 @@ struct NsConfig {
   static constexpr bool B_MN = KIND == kNsApply;       // X as [k, n]: its columns are contiguous
   static constexpr int OP_BYTES = BM * BK * 2;         // 16 KB of each operand a CTA and stage
   static constexpr int STAGE_BYTES = 2 * OP_BYTES;
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = SPLIT ? 4 : 6;
   static constexpr int NUM_BUFS = 2;
   static constexpr int THREADS = 320;                  // producer, MMA issuer, 8 epilogue warps
-  static constexpr int TURN_BYTES = KIND_ == kNsApply ? 8 * 32 * 33 * 4 : 0;  // a block an epilogue warp
+  // kNsApply: a block an epilogue warp; SPLIT: the parts of this CTA's rows, 128 x 128 fp32 in all.
+  static constexpr int TURN_BYTES = KIND_ == kNsApply ? 8 * 32 * 33 * 4 : SPLIT ? 128 * 128 * 4 : 0;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256 + TURN_BYTES;
   static constexpr uint32_t IDESC = umma_idesc_f16(PAIR ? 256 : 128, TILE, false, B_MN);
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per block");
+  static_assert(!SPLIT || (SYMMETRIC && !PAIR), "split over K: symmetric products on single SMs");
 };
 
 struct NsUnit {
@@ -228,10 +242,11 @@ __device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int co
     if (row < p.m && e < cols) p.W[static_cast<long long>(col + e) * p.m + row] = fmaf(p.keep, w[e], -p.rate * turn[lane][e]);
 }
 
-// One epilogue warp's 32 x 32 block of A or B: rows r0 .. (this thread's is r0 + lane), columns col ...
-template <class Cfg>
+// One epilogue warp's 32 x 32 block of A or B: rows r0 .. (this thread's is r0 + lane), columns col ..;
+// `product` fills in this thread's 32 values of the product.
+template <class Cfg, typename Product>
 __device__ __forceinline__ void ns_symmetric_block(const NsParams& p, const NsUnit& w, int r0, int col, int cols,
-                                                   uint32_t tacc, uint32_t lane, float delta, float& tr) {
+                                                   Product product, uint32_t lane, float delta, float& tr) {
   const int r = r0 + static_cast<int>(lane);
   const bool row_ok = r < p.m;
   const long long at = static_cast<long long>(r) * p.n + col;
@@ -244,9 +259,7 @@ __device__ __forceinline__ void ns_symmetric_block(const NsParams& p, const NsUn
       if (row_ok && 8 * q < cols) a4[q] = *reinterpret_cast<const uint4*>(p.A + at + 8 * q);
     }
   }
-  __syncwarp();
-  tmem_ld32(tacc, v);
-  tmem_ld_wait();
+  product(v);
   if constexpr (Cfg::KIND == kNsPoly) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -301,7 +314,14 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsUnit& w, 
       if (c0 + 32 < (half + 1) * (Cfg::TILE / 2)) ns_load_planes(p, r0, col + 32, lane, ahead);
       ns_apply_block(p, r0, col, cols, tacc + c0, turn, lane, kNsA + delta, old);
     } else
-      ns_symmetric_block<Cfg>(p, w, r0, col, cols, tacc + c0, lane, delta, tr);
+      ns_symmetric_block<Cfg>(
+          p, w, r0, col, cols,
+          [&](float(&v)[32]) {
+            __syncwarp();
+            tmem_ld32(tacc + c0, v);
+            tmem_ld_wait();
+          },
+          lane, delta, tr);
     __syncwarp();
   }
   if constexpr (Cfg::KIND == kNsGram) {
@@ -326,14 +346,20 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  constexpr bool PAIR = Cfg::PAIR;
+  constexpr bool PAIR = Cfg::PAIR, SPLIT = Cfg::SPLIT;
   constexpr int kCtas = PAIR ? 2 : 1;
   const int warp = threadIdx.x / 32;
   const uint32_t lane = lane_id();
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
   const bool leader = rank == 0;
-  const int first = blockIdx.x / kCtas;
-  const int step = gridDim.x / kCtas;
+  // SPLIT: one unit a cluster, whose CTA `share` of `shares` takes K blocks kb_begin .. kb_end.
+  const int shares = SPLIT ? static_cast<int>(cluster_size()) : 1;
+  const int share = SPLIT ? static_cast<int>(cluster_rank()) : 0;
+  const int first = SPLIT ? blockIdx.x / shares : blockIdx.x / kCtas;
+  const int step = SPLIT ? p.num_units : gridDim.x / kCtas;
+  const int kb_share = (p.k_blocks + shares - 1) / shares;
+  const int kb_begin = share * kb_share < p.k_blocks ? share * kb_share : p.k_blocks;
+  const int kb_end = kb_begin + kb_share < p.k_blocks ? kb_begin + kb_share : p.k_blocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
@@ -361,7 +387,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
     tc_fence_before();
   }
   __syncthreads();
-  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers exist before any remote arrival
+  if constexpr (PAIR || SPLIT) cluster_sync_all();  // every CTA runs, and its barriers exist, before remote accesses
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();  // barriers and TMEM are ready; global memory only from here
@@ -378,7 +404,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
         const NsUnit w = ns_unit<Cfg>(p, u);
         const int a0 = w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
         const int b0 = w.nb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;  // its half of B (PAIR), all of it else
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           if (!mbar_wait_bounded(smem_addr(empty + stage), phase ^ 1u, abort_flag, p.status, 21u)) {
             ok = false;
             break;
@@ -425,7 +451,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
         if (!mbar_wait_bounded(smem_addr(acc_empty + buf), buf_phase ^ 1u, abort_flag, p.status, 22u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + buf * 256;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           if (!mbar_wait_bounded(smem_addr(full + stage), phase, abort_flag, p.status, 23u)) {
             ok = false;
             break;
@@ -440,9 +466,9 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
                                           : umma_desc_sw128(sB + ks * 32, 16, 1024);
             // (These issue tcgen05.mma kind::f16; the instruction descriptor says fp16 operands.)
             if constexpr (PAIR)
-              umma_bf16_pair(d_tmem, da, db, Cfg::IDESC, (kb > 0 || ks > 0) ? 1u : 0u);
+              umma_bf16_pair(d_tmem, da, db, Cfg::IDESC, (kb > kb_begin || ks > 0) ? 1u : 0u);
             else
-              umma_bf16(d_tmem, da, db, Cfg::IDESC, (kb > 0 || ks > 0) ? 1u : 0u);
+              umma_bf16(d_tmem, da, db, Cfg::IDESC, (kb > kb_begin || ks > 0) ? 1u : 0u);
           }
           if constexpr (PAIR)
             umma_commit_pair(smem_addr(empty + stage), 0x3);
@@ -476,6 +502,26 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
         }
       }
     }
+  } else if constexpr (SPLIT) {
+    // ------------------------------------------------------------ this CTA's part of the tile to the owners
+    const int wq = warp & 3, half = (warp - 2) >> 2;
+    const bool ok = mbar_wait_bounded(smem_addr(acc_full), 0u, abort_flag, p.status, 24u);
+    tc_fence_after();
+    const int rows = 128 / shares, owner = 32 * wq / rows, row = 32 * wq % rows + static_cast<int>(lane);
+    // parts[share][column][row]: a column of the warp's 32 rows is 128 contiguous bytes.
+    const uint32_t to = map_to_rank(smem_addr(smem + Cfg::STAGES * Cfg::STAGE_BYTES + 256), owner) +
+                        static_cast<uint32_t>((share * 128 + 64 * half) * rows + row) * 4u;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      float v[32];
+      __syncwarp();
+      tmem_ld32(tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + 64 * half + 32 * part, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        st_cluster_f32(to + static_cast<uint32_t>((32 * part + e) * rows) * 4u, ok && kb_end > kb_begin ? v[e] : 0.0f);
+    }
+    tc_fence_before();
   } else {
     // ------------------------------------------------------------ epilogue warps 2..9 (every CTA)
     const int wq = warp & 3;           // TMEM lane quarter this warp may access
@@ -504,6 +550,36 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
       if (++buf == Cfg::NUM_BUFS) {
         buf = 0;
         buf_phase ^= 1u;
+      }
+    }
+  }
+  if constexpr (SPLIT) {
+    __syncthreads();
+    cluster_sync_all();  // every part of this CTA's rows has arrived, and nothing is sent after it
+    const int rows = 128 / shares, ew = warp - 2;
+    // 32 x 32 blocks of the owned rows, one a warp: rows / 32 x 4 of them, at most 8.
+    if (ew >= 0 && ew < rows / 32 * 4) {
+      const NsUnit w = ns_unit<Cfg>(p, first);
+      const int rb = ew / 4 * 32, c0 = ew % 4 * 32;
+      const int r0 = w.mb * 128 + share * rows + rb, col = w.nb * 128 + c0, cols = min(32, p.n - col);
+      const float* parts = reinterpret_cast<const float*>(smem + Cfg::STAGES * Cfg::STAGE_BYTES + 256);
+      const float delta = Cfg::KIND == kNsGram ? 0.0f : ns_delta(p.trace, p.order, lane);
+      float tr = 0.0f;
+      if (cols > 0)
+        ns_symmetric_block<Cfg>(
+            p, w, r0, col, cols,
+            [&](float(&v)[32]) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+              for (int s = 0; s < shares; ++s)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] += parts[(s * 128 + c0 + e) * rows + rb + static_cast<int>(lane)];
+            },
+            lane, delta, tr);
+      __syncwarp();
+      if (Cfg::KIND == kNsGram && r0 == col) {  // the block on the diagonal
+        tr = warp_sum(tr);
+        if (lane == 0 && r0 < p.m) p.trace[r0 / 32] = tr;
       }
     }
   }
@@ -556,14 +632,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 __device__ __forceinline__ void st_cluster_16(uint32_t addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -640,6 +708,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
     tc_fence_before();
   }
   __syncthreads();
+  if (ctas > 1) cluster_sync_all();  // every CTA runs before its shared memory is written from others
   tc_fence_after();
   const uint32_t tm_x = tmem_slot + (static_cast<uint32_t>(32 * (warp % 4)) << 16);  // X, 256 columns
   const uint32_t tm_acc = tm_x + 256;                                                // the product at hand

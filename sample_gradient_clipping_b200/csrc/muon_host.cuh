@@ -58,7 +58,7 @@ dp_status map_f16(CUtensorMap* map, const __half* base, int rows, int cols, uint
 }
 
 template <class Cfg>
-dp_status launch_ns(NsParams p, cudaStream_t stream) {
+dp_status launch_ns(NsParams p, cudaStream_t stream, int shares = 1) {
   auto kernel = [] {
     if constexpr (Cfg::PAIR)
       return ns_pair_kernel<Cfg>;
@@ -73,10 +73,10 @@ dp_status launch_ns(NsParams p, cudaStream_t stream) {
     if (dev >= 0 && dev < 64) configured[dev].store(true);
   }
   const int ctas = Cfg::PAIR ? 2 : 1;
-  const int grid = std::min(p.num_units, sm_count() / ctas) * ctas;
+  const int grid = Cfg::SPLIT ? p.num_units * shares : std::min(p.num_units, sm_count() / ctas) * ctas;
   p.early = 2 * grid <= sm_count() ? 1 : 0;
   LaunchScope scope(kKindNsProduct, stream);
-  DP_LAUNCH("ns_kernel", kernel, grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
+  DP_LAUNCH_CLUSTER("ns_kernel", Cfg::SPLIT ? shares : 0, kernel, grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
   return DP_OK;
 }
 
@@ -96,6 +96,18 @@ dp_status ns_product(NsParams p, cudaStream_t stream) {
   p.tiles_m = pair ? tm2 : tm1;
   p.tiles_n = pair ? tn2 : tn1;
   p.num_units = pair ? u2 : u1;
+  if constexpr (KIND != kNsApply) {
+    // Few tiles: their K blocks (0.28 us each) are shared by 4 or 2 SMs a tile, where that saves more
+    // than the exchange of the parts costs (about 2 us).  Clusters of 4 leave some SMs of a group unused:
+    // 36 of them did not fit at once (1024 x 1024: 193 us against 140 unsplit), 32 do.
+    const int shares = u1 * 4 <= 128 && p.k_blocks >= 16 ? 4 : u1 * 2 <= sm_count() && p.k_blocks >= 24 ? 2 : 1;
+    if (shares > 1) {
+      p.tiles_m = tm1;
+      p.tiles_n = tn1;
+      p.num_units = u1;
+      return launch_ns<NsConfig<false, KIND, true>>(p, stream, shares);
+    }
+  }
   return pair ? launch_ns<NsConfig<true, KIND>>(p, stream) : launch_ns<NsConfig<false, KIND>>(p, stream);
 }
 

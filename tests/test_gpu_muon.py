@@ -63,7 +63,8 @@ def _matrix(m, n, kind, seed):
 
 SHAPES = [(8, 8), (8, 200), (200, 8), (64, 32), (128, 128), (136, 120), (264, 264), (128, 1024), (1024, 128),
           (16, 256), (40, 264), (128, 512), (72, 520), (2048, 120), (104, 2056), (4096, 128), (24, 4104), (128, 1416), (88, 1992),
-          (520, 1400), (1400, 520), (1096, 1096)]
+          (520, 1400), (1400, 520), (1096, 1096),
+          (136, 2000), (1544, 264), (1032, 1096), (1160, 1544)]   # symmetric products split over 4 and 2 SMs a tile
 
 
 def _check(G_h, G_d, steps=5):
