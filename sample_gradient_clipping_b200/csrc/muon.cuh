@@ -68,6 +68,14 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ uint4 pack_half8(const float* v) {
+  uint4 q;
+  __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+  return q;
+}
+
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4)                                 // D: f32; A and B format 0: f16
          | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -91,8 +99,8 @@ struct NsConfig {
   static constexpr int STAGES = SPLIT ? 4 : 6;
   static constexpr int NUM_BUFS = 2;
   static constexpr int THREADS = 320;                  // producer, MMA issuer, 8 epilogue warps
-  // kNsApply: a block an epilogue warp; SPLIT: the parts of this CTA's rows, 128 x 128 fp32 in all.
-  static constexpr int TURN_BYTES = KIND_ == kNsApply ? 8 * 32 * 33 * 4 : SPLIT ? 128 * 128 * 4 : 0;
+  // A block an epilogue warp; SPLIT: the parts of this CTA's rows, 128 x 128 fp32 in all.
+  static constexpr int TURN_BYTES = SPLIT ? 128 * 128 * 4 : 8 * 32 * 33 * 4;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256 + TURN_BYTES;
   static constexpr uint32_t IDESC = umma_idesc_f16(PAIR ? 256 : 128, TILE, false, B_MN);
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per block");
@@ -242,59 +250,72 @@ __device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int co
     if (row < p.m && e < cols) p.W[static_cast<long long>(col + e) * p.m + row] = fmaf(p.keep, w[e], -p.rate * turn[lane][e]);
 }
 
-// One epilogue warp's 32 x 32 block of A or B: rows r0 .. (this thread's is r0 + lane), columns col ..;
-// `product` fills in this thread's 32 values of the product.
+// One epilogue warp's 32 x 32 block of A or B, turned through shared memory like X's: `product` gives
+// this thread's 32 values of the product (row r0 + lane, columns col ..).  Rows and, off the diagonal,
+// the same values as rows of the tile below it, are written in runs of 64 bytes.
 template <class Cfg, typename Product>
 __device__ __forceinline__ void ns_symmetric_block(const NsParams& p, const NsUnit& w, int r0, int col, int cols,
-                                                   Product product, uint32_t lane, float delta, float& tr) {
-  const int r = r0 + static_cast<int>(lane);
-  const bool row_ok = r < p.m;
-  const long long at = static_cast<long long>(r) * p.n + col;
-  float v[32];
+                                                   Product product, float (*turn)[33], uint32_t lane, float delta,
+                                                   float& tr) {
+  const int lr = static_cast<int>(lane) / 4, lc = static_cast<int>(lane) % 4 * 8;
   [[maybe_unused]] uint4 a4[4];
   if constexpr (Cfg::KIND == kNsPoly) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      a4[q] = make_uint4(0u, 0u, 0u, 0u);
-      if (row_ok && 8 * q < cols) a4[q] = *reinterpret_cast<const uint4*>(p.A + at + 8 * q);
+    for (int k = 0; k < 4; ++k) {
+      const int row = r0 + 8 * k + lr;
+      a4[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < p.m && lc < cols) a4[k] = *reinterpret_cast<const uint4*>(p.A + static_cast<long long>(row) * p.n + col + lc);
     }
   }
-  product(v);
-  if constexpr (Cfg::KIND == kNsPoly) {
+  {
+    float v[32];
+    product(v);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const __half2* h = reinterpret_cast<const __half2*>(&a4[q]);
+    for (int e = 0; e < 32; ++e) turn[lane][e] = v[e];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = 8 * k + lr, row = r0 + i;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = turn[i][lc + e];
+    if constexpr (Cfg::KIND == kNsPoly) {
+      const __half2* h = reinterpret_cast<const __half2*>(&a4[k]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 a = __half22float2(h[e]);
-        v[8 * q + 2 * e] = fmaf(kNsB, a.x, kNsC * v[8 * q + 2 * e]);
-        v[8 * q + 2 * e + 1] = fmaf(kNsB, a.y, kNsC * v[8 * q + 2 * e + 1]);
+        x[2 * e] = fmaf(kNsB, a.x, kNsC * x[2 * e]);
+        x[2 * e + 1] = fmaf(kNsB, a.y, kNsC * x[2 * e + 1]);
       }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    if (col + e != r) continue;
-    if constexpr (Cfg::KIND == kNsPoly)
-      v[e] -= delta;
-    else
-      tr = v[e];
-  }
-  if (!row_ok) return;
+    for (int e = 0; e < 8; ++e) {
+      if (col + lc + e != row) continue;
+      if constexpr (Cfg::KIND == kNsPoly)
+        x[e] -= delta;
+      else
+        tr += x[e];
+    }
+    if constexpr (Cfg::KIND == kNsPoly) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (8 * q >= cols || !DP_DCHECK(at + 8 * q + 8 <= static_cast<long long>(p.m) * p.n, 62u, p.status)) break;
-    uint4 h4;
-    __half2* h = reinterpret_cast<__half2*>(&h4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-    *reinterpret_cast<uint4*>(p.out + at + 8 * q) = h4;
+      for (int e = 0; e < 8; ++e) turn[i][lc + e] = x[e];
+    }
+    const long long at = static_cast<long long>(row) * p.n + col + lc;
+    if (row < p.m && lc < cols && DP_DCHECK(at + 8 <= static_cast<long long>(p.m) * p.n, 62u, p.status))
+      *reinterpret_cast<uint4*>(p.out + at) = pack_half8(x);
   }
   if (w.mb == w.nb) return;
-  // The tile below the diagonal: column e of this one is its row, the warp's 32 rows a run of 64 bytes.
+  __syncwarp();
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (e < cols) p.out[static_cast<long long>(col + e) * p.m + r] = __float2half_rn(v[e]);
+  for (int k = 0; k < 4; ++k) {  // column 8 k + lr of the block, its rows lc .. lc + 7
+    const int i = 8 * k + lr;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = turn[lc + e][i];
+    if (i < cols && r0 + lc < p.m)
+      *reinterpret_cast<uint4*>(p.out + static_cast<long long>(col + i) * p.m + r0 + lc) = pack_half8(x);
+  }
 }
 
 // This epilogue warp's share of a unit: 32 rows from r0, half the tile's columns.
@@ -321,7 +342,7 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsUnit& w, 
             tmem_ld32(tacc + c0, v);
             tmem_ld_wait();
           },
-          lane, delta, tr);
+          turn, lane, delta, tr);
     __syncwarp();
   }
   if constexpr (Cfg::KIND == kNsGram) {
@@ -575,7 +596,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] += parts[(s * 128 + c0 + e) * rows + rb + static_cast<int>(lane)];
             },
-            lane, delta, tr);
+            reinterpret_cast<float(*)[33]>(smem) + 32 * ew, lane, delta, tr);  // the ring's stages are free
       __syncwarp();
       if (Cfg::KIND == kNsGram && r0 == col) {  // the block on the diagonal
         tr = warp_sum(tr);
@@ -664,14 +685,6 @@ constexpr int kNsSmallSmem = 1024 + (kNsSmallMaxChunks + 4) * kNsTile + kNsSmall
 // 16-byte unit `unit` (of 8) of row r in a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t ns_unit_offset(int r, int unit) {
   return static_cast<uint32_t>(r * 128 + ((unit ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ uint4 pack_half8(const float* v) {
-  uint4 q;
-  __half2* h = reinterpret_cast<__half2*>(&q);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-  return q;
 }
 
 template <typename T, bool MUON>
