@@ -316,7 +316,9 @@ dp_status dp_projected_adam_step(float* W, const float* R, float* m, float* v, c
  *     padding_idx = -1 (or any value that is no id): no padding row.
  *   - d is a multiple of 8 (bf16) or 4 (fp32); B*T < 2^31; V*d <= 2^34; scale is finite.
  *   - Results are the same bits on every run.  A row that no token names gets the noise alone
- *     (the noise of a private step covers every row). */
+ *     (the noise of a private step covers every row).
+ *   - A workspace serves one call at a time: calls that may overlap (other streams, graphs replayed
+ *     beside each other) each need their own.  So it is for the calls further below. */
 
 /* Y[n] = scale W[ids[n]] for n < N, formed in fp32 and rounded once; ids outside [0, V) give a
  * row of zeros.  (The padding row is looked up like any other.)
@@ -399,7 +401,8 @@ dp_status dp_rmsnorm_step(const void* H, const float* gain, const void* dY, cons
                           unsigned long long seed, unsigned long long step, unsigned layer_id, void* dX,
                           float* norms_out, float* G_out, void* workspace, size_t ws_bytes, void* stream);
 
-/* dp_rmsnorm_step with the step number in device memory. */
+/* dp_rmsnorm_step with the step number in device memory (capture after one ordinary call, as for
+ * dp_linear_step_dev_step). */
 dp_status dp_rmsnorm_step_dev_step(const void* H, const float* gain, const void* dY,
                                    const void* residual_grad, dp_dtype dt, int B, int T, int d, float eps,
                                    float C, float sigma, unsigned long long seed,
@@ -421,7 +424,7 @@ dp_status dp_rmsnorm_step_dev_step(const void* H, const float* gain, const void*
  *   - Dimensions are multiples of 8, at least 8; rows*cols <= 2^34, the smaller <= 65536;
  *     1 <= steps <= 32.
  *   - A matrix of zeros gives zeros; infinities or NaN in it give NaN.
- *   - Results are the same bits on every run. */
+ *   - Results are the same bits on every run.  Capture after one ordinary call of the same shape. */
 
 /* Workspace bytes of both calls: 8 rows*cols + 4 min(rows, cols)^2 and a little (0 when the
  * shape is invalid). */

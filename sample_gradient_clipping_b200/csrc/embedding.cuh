@@ -494,12 +494,13 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
 constexpr int kEmbVecs = 2;
 constexpr int kEmbWindow = 16;  // sorted positions whose groups a warp takes
 
-// blockIdx.y: chunk.  Long groups first, each by a block whose warps share its rows.  Then each warp
+// blockIdx.y: chunk.  Long groups first, each by a block whose warps share its rows (all there is to do
+// when the norms are given: `short_groups` false).  Then each warp
 // takes the short groups that start among 16 positions: these end within 32, so one load of the
 // order shows them all, and their rows are added as one stream, cut where a group ends.
 template <typename T>
 __global__ void __launch_bounds__(kEmbThreads, 4)
-    emb_norm_kernel(const T* __restrict__ dY, long long N, int V_rows, int d, EmbIndex ix) {
+    emb_norm_kernel(const T* __restrict__ dY, long long N, int V_rows, int d, bool short_groups, EmbIndex ix) {
   griddep_enter();
   constexpr int V = EmbVec<T>::N;
   constexpr int kCols = 32 * V * kEmbVecs;
@@ -587,6 +588,7 @@ __global__ void __launch_bounds__(kEmbThreads, 4)
     __syncthreads();
   }
 
+  if (!short_groups) return;
   const uint32_t none = static_cast<uint32_t>(V_rows);
   const long long windows = (N + kEmbWindow - 1) / kEmbWindow;
   for (long long w = static_cast<long long>(blockIdx.x) * kEmbWarps + warp; w < windows;

@@ -117,15 +117,15 @@ dp_status emb_sort(const EmbCall& s, const EmbLayout& L, const EmbIndex& ix, int
   return DP_OK;
 }
 
-dp_status emb_group_sums(const EmbCall& s, const EmbIndex& ix, const void* dY, cudaStream_t stream) {
+dp_status emb_group_sums(const EmbCall& s, const EmbIndex& ix, const void* dY, bool short_groups, cudaStream_t stream) {
   const dim3 grid = emb_grid(s.norm_chunks(), (s.N() + kEmbWindow - 1) / kEmbWindow, 8);
   LaunchScope scope(kKindEmbNorm, stream);
   if (s.dt == DP_BF16) {
     DP_LAUNCH("emb_norm_kernel", emb_norm_kernel<__nv_bfloat16>, grid, kEmbThreads, 0, stream,
-              static_cast<const __nv_bfloat16*>(dY), s.N(), s.V, s.d, ix);
+              static_cast<const __nv_bfloat16*>(dY), s.N(), s.V, s.d, short_groups, ix);
   } else {
     DP_LAUNCH("emb_norm_kernel", emb_norm_kernel<float>, grid, kEmbThreads, 0, stream, static_cast<const float*>(dY),
-              s.N(), s.V, s.d, ix);
+              s.N(), s.V, s.d, short_groups, ix);
   }
   return DP_OK;
 }
@@ -231,7 +231,7 @@ dp_status embedding_step(const void* ids, dp_index it, const void* dY, dp_dtype 
   float* norms = reinterpret_cast<float*>(ws + L.norms);
   const double noise_std = (sigma == 0.0f) ? 0.0 : static_cast<double>(sigma) * static_cast<double>(C);
   if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
-  if ((st = emb_group_sums(s, ix, dY, cs)) != DP_OK) return st;
+  if ((st = emb_group_sums(s, ix, dY, true, cs)) != DP_OK) return st;
   if ((st = emb_norms(s, ix, scale, norms, norms_out, cs)) != DP_OK) return st;
   return emb_sum(s, ix, dY, norms, C, scale, false, noise_std, seed, step, layer_id, G_out, cs);
 }
@@ -276,7 +276,7 @@ dp_status dp_embedding_per_sample_norms(const void* ids, dp_index it, const void
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const EmbIndex ix = emb_index(s, L, ws, passes);
   if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
-  if ((st = emb_group_sums(s, ix, dY, cs)) != DP_OK) return st;
+  if ((st = emb_group_sums(s, ix, dY, true, cs)) != DP_OK) return st;
   return emb_norms(s, ix, scale, nullptr, norms, cs);
 }
 
@@ -295,7 +295,7 @@ dp_status dp_embedding_clip_accumulate(const void* ids, dp_index it, const void*
   const EmbIndex ix = emb_index(s, L, ws, passes);
   if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
   // The long groups' sums are the norm kernel's; the norms themselves are the caller's.
-  if ((st = emb_group_sums(s, ix, dY, cs)) != DP_OK) return st;
+  if ((st = emb_group_sums(s, ix, dY, false, cs)) != DP_OK) return st;
   return emb_sum(s, ix, dY, norms, C, scale, true, 0.0, 0, step_value(0), 0, G_sum, cs);
 }
 

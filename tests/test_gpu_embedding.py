@@ -76,6 +76,8 @@ SHAPES = [
     (1, 1, 1, 8), (1, 1, 70000, 16), (3, 5, 1, 8), (2, 31, 7, 24), (2, 33, 7, 264), (4, 16, 512, 64),
     (5, 333, 40, 136), (2, 700, 3, 520), (9, 257, 255, 72), (9, 257, 256, 72), (3, 129, 65535, 40), (3, 129, 65536, 40),
     (70, 40, 11, 16), (1, 4099, 300, 32), (16, 1031, 261, 104),
+    # more tokens than a pass of the sort keeps in registers, in one digit and in three
+    (5, 9001, 200, 8), (1, 70001, 70000, 8),
 ]
 
 
@@ -85,6 +87,42 @@ def test_step_matches_the_oracle(shape, dt):
     B, T, V, d = shape
     _check(B, T, V, d, dt, seed=sum(shape), sigma=0.7 if V * d < 2_000_000 else 0.0, scale=0.5,
            index="int32" if d % 16 else "int64")
+
+
+@pytest.mark.parametrize("first", [0, 5, 17, 31])
+def test_group_and_row_lengths_around_the_thresholds(first):
+    """Groups of 1 to 130 tokens of one id, alone and as rows of several samples, at every phase of the
+    windows of 16 and 32 positions in which the order is read."""
+    lengths = [1, 2, 15, 16, 17, 18, 31, 32, 33, 47, 48, 49, 63, 64, 65, 66, 96, 130]
+    T = first + sum(lengths)
+    one = np.concatenate([np.arange(first)] + [np.full(n, first + k) for k, n in enumerate(lengths)])
+    rng = np.random.default_rng(first)
+    # Two samples with the same ids in different orders, and one that has each id once or not at all.
+    ids = np.stack([rng.permutation(one), rng.permutation(one), np.arange(T) % 60])
+    _check(3, T, 60, 72, "bf16", seed=first, ids=lambda _: ids, sigma=0.3)
+
+
+def test_offsets_past_32_bits():
+    """A table, an output and a gradient of more than 2^31 elements: the far rows are found."""
+    d, V, N = 4096, 530_000, 530_000
+    W = torch.zeros(V, d, dtype=torch.bfloat16, device="cuda")
+    far = [V - 1, V - 2, 524_288, 262_144, 1]
+    for k, v in enumerate(far):
+        W[v] = k + 1
+    y = _lib.dp_embedding_lookup(W, torch.tensor(far, device="cuda"))
+    assert [float(r.min()) for r in y] == [float(r.max()) for r in y] == [1, 2, 3, 4, 5]
+    ids = torch.zeros(1, N, dtype=torch.int32, device="cuda")
+    ids[0, -3:] = torch.tensor([7, 9, 7], dtype=torch.int32)
+    W.zero_()
+    dY = W.view(1, N, d)
+    dY[0, -3:] = torch.tensor([[1.0], [2.0], [4.0]], device="cuda").to(torch.bfloat16)
+    G, n = _lib.dp_embedding_step(ids, dY, 12, 1000.0, 0.0, 0, 0, 0)
+    assert abs(float(n[0]) - np.sqrt(d * 29.0)) <= 1e-3
+    assert float(G[7].min()) == float(G[7].max()) == 5.0 and float(G[9].min()) == 2.0 == float(G[9].max())
+    assert float(G[:7].abs().max()) == 0.0
+    # and the output of a lookup past 2^31 elements
+    Y = _lib.dp_embedding_lookup(torch.arange(12, device="cuda").to(torch.bfloat16)[:, None].expand(12, d).contiguous(), ids, out=dY)
+    assert [float(v) for v in Y[0, -4:, 0]] == [0.0, 7.0, 9.0, 7.0]
 
 
 def test_narrow_fp32_rows():

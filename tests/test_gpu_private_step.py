@@ -184,3 +184,29 @@ def test_checked_build_gives_the_same_bits():
     with _lib.using(_lib.debug_lib()):
         got = run()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refused_launches_are_reported_and_the_next_call_is_whole():
+    """Each launch of each call refused in turn, on the host: the call reports it and enqueues no
+    more, and the same call then gives the bits of an undisturbed one."""
+    p, ids, r, dz = _model(4)
+    e, g, _ = _backward(p, ids, r, dz)
+    G = torch.sin(torch.arange(200 * 328, device="cuda", dtype=torch.float32)).reshape(200, 328)
+    calls = [lambda: _lib.dp_embedding_step(e["ids"], e["dY"], V, 0.3, 0.5, SEED, STEP, 0),
+             lambda: (_lib.dp_embedding_lookup(p["E"].cuda(), e["ids"]),),
+             lambda: _lib.dp_rmsnorm(g["H"], g["gain"]),
+             lambda: _lib.dp_rmsnorm_step(g["H"], g["gain"], g["dY"], 0.3, 0.5, SEED, STEP, 1),
+             lambda: (_lib.dp_orthogonalize(G),), lambda: (_lib.dp_orthogonalize(G[:64].contiguous()),)]
+    for call in calls:
+        n = _lib.kernel_launches()
+        want = call()
+        n = _lib.kernel_launches() - n
+        for k in range(n):
+            try:
+                assert _lib.lib().dp_selftest_fail_launches(k, 1, 2) == _lib.DP_OK     # cudaErrorMemoryAllocation
+                with pytest.raises(_lib.DPError) as err:
+                    call()
+                assert err.value.status == _lib.DP_ERR_CUDA and "memory" in str(err.value)
+            finally:
+                _lib.lib().dp_selftest_fail_launches(0, 0, 0)
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))

@@ -123,6 +123,24 @@ def test_many_samples():
     assert np.all(np.abs(host(G) - ref["out"]) <= bS)
 
 
+def test_offsets_past_32_bits():
+    d, B, T = 4096, 5, 106_000
+    H = torch.zeros(B, T, d, dtype=torch.bfloat16, device="cuda")
+    dY = torch.zeros_like(H)
+    H[4, -1, ::2] = 2.0
+    H[4, -1, 1::2] = -2.0
+    dY[4, -1] = 1.0
+    gain = torch.full((d,), 3.0, device="cuda")
+    dX, G, n = _lib.dp_rmsnorm_step(H, gain, dY, 1e6, 0.0, 0, 0, 0, eps=1e-5)
+    # r = 1/2 up to eps, u.h sums to zero: dX = r g dy, and the gain's gradient is dy h r = +-1.
+    assert torch.all((dX[4, -1] - 1.5).abs() <= 2 ** -8 * 1.5) and float(dX[:4].abs().max()) == 0.0
+    assert torch.all((G.abs() - 1.0).abs() <= 1e-5) and float(G[0]) > 0 > float(G[1]) and float(n[:4].max()) == 0.0
+    assert abs(float(n[4]) - 64.0) <= 1e-3
+    del dX
+    Y, _ = _lib.dp_rmsnorm(H, gain, eps=1e-5, Y=dY)
+    assert torch.all((Y[4, -1].abs() - 3.0).abs() <= 2 ** -8 * 3.0) and float(Y[4, -2].abs().max()) == 0.0
+
+
 def test_gradients_against_differences():
     """The backward of the forward that is called, by central differences in fp32."""
     h_h, h, y_h, y, gain_h, gain = _draw(1, 2, 16, "f32", 9, n=2)
