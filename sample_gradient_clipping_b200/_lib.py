@@ -183,14 +183,19 @@ def check(status, what):
         raise DPError(status, what)
 
 
-def _dtype_code(t):
-    import torch
+_DTYPE_CODES = {}   # torch dtype -> dp_dtype, filled on the first use (torch is imported lazily)
 
-    if t.dtype == torch.bfloat16:
-        return DP_BF16
-    if t.dtype == torch.float32:
-        return DP_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+
+def _dtype_code(t):
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        import torch
+
+        _DTYPE_CODES.update({torch.bfloat16: DP_BF16, torch.float32: DP_F32})
+        code = _DTYPE_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _stream(stream):
@@ -451,16 +456,12 @@ class _Launch:
         import torch
 
         index = self.index = tensors[0].get_device()
-        for name, t in zip(names.split(), tensors):
-            if t is None:
-                continue
-            at = t.get_device()
-            if at < 0:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            if at != index:
-                raise ValueError(f"{name} is on {t.device}, the first tensor on {tensors[0].device}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+        ok = index >= 0
+        for t in tensors:
+            if t is not None and (t.get_device() != index or not t.is_contiguous()):
+                ok = False
+        if not ok:
+            self._complain(names, tensors)
         self.ctx = None
         if stream is not None:   # also makes the stream's device current
             if isinstance(stream, int):
@@ -470,6 +471,17 @@ class _Launch:
             self.ctx = torch.cuda.stream(stream)
         elif index != torch.cuda.current_device():
             self.ctx = torch.cuda.device(index)
+
+    @staticmethod
+    def _complain(names, tensors):
+        for name, t in zip(names.split(), tensors):
+            if t is not None:
+                if not t.is_cuda:
+                    raise ValueError(f"{name} must be a CUDA tensor")
+                if t.device != tensors[0].device:
+                    raise ValueError(f"{name} is on {t.device}, the first tensor on {tensors[0].device}")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
 
     def __enter__(self):
         if self.ctx is not None:
@@ -482,13 +494,19 @@ class _Launch:
         return False
 
 
+_short_stream = None
+
+
 def _raw_stream(index):
     """The handle of the device's current stream (the short way to it where torch has one: a
     Stream object costs 3 us, a third of a small call)."""
-    import torch
+    global _short_stream
+    if _short_stream is None:
+        import torch
 
-    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return short(index) if short is not None else torch.cuda.current_stream(index).cuda_stream
+        _short_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _short_stream(index)
 
 
 def _expect(t, name, shape, dtype):

@@ -630,15 +630,38 @@ __global__ void __launch_bounds__(kEmbThreads, 4)
   }
 }
 
-// norms[i] = |scale| sqrt(sum of the sample's T * chunks slots): one block a sample, fp64, in a
-// fixed order.
+// |scale| sqrt(sum of a sample's slots), in fp64, by one warp in a fixed order.
+__device__ __forceinline__ float emb_norm_by_warp(const float* __restrict__ slots, long long count, float scale,
+                                                  uint32_t lane) {
+  double acc = 0.0;
+#pragma unroll 4
+  for (long long k = lane; k < count; k += 32) acc += static_cast<double>(slots[k]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
+  return static_cast<float>(fabs(static_cast<double>(scale)) * sqrt(acc));
+}
+
+// norms[i] = |scale| sqrt(sum of the sample's T * chunks slots): one block a sample, in a fixed order.
+// `by_warp`: in the order above, by one warp, which is what the sum kernel does for itself in small
+// calls (kEmbSmallSlots), so that every entry point gives a shape's norms in the same bits.
 constexpr int kEmbNormThreads = 512;
+constexpr long long kEmbSmallSlots = 8192;
+constexpr int kEmbSmallSamples = 64;
 __global__ void __launch_bounds__(kEmbNormThreads)
-    emb_norms_kernel(const float* __restrict__ sq, long long per_sample, float scale, float* __restrict__ norms,
-                     float* __restrict__ norms_out) {
+    emb_norms_kernel(const float* __restrict__ sq, long long per_sample, float scale, bool by_warp,
+                     float* __restrict__ norms, float* __restrict__ norms_out) {
   griddep_enter();
   __shared__ double part[kEmbNormThreads / 32];
   const float* mine = sq + static_cast<long long>(blockIdx.x) * per_sample;
+  if (by_warp) {
+    if (threadIdx.x >= 32) return;
+    const float n = emb_norm_by_warp(mine, per_sample, scale, threadIdx.x);
+    if (threadIdx.x == 0) {
+      if (norms) norms[blockIdx.x] = n;
+      if (norms_out) norms_out[blockIdx.x] = n;
+    }
+    return;
+  }
   double acc = 0.0;
 #pragma unroll 8
   for (long long k = threadIdx.x; k < per_sample; k += kEmbNormThreads) acc += static_cast<double>(mine[k]);
@@ -667,7 +690,7 @@ __device__ __forceinline__ float4 fma4(float c, float4 x, float4 a) {
 // acc += scale c_i (token's row, or long group's sum) over the sorted positions first .. end.
 template <typename T>
 __device__ __forceinline__ void emb_add_clipped(const T* __restrict__ dY, const EmbIndex& ix, uint32_t first,
-                                                uint32_t end, uint32_t T_len, const float* __restrict__ norms, float C,
+                                                uint32_t end, uint32_t T_len, const float* norms, float C,
                                                 float scale, int d, int col, uint32_t lane, float4 (&acc)[kEmbQuads<T>]) {
   constexpr int Q = kEmbQuads<T>;
   constexpr int kU = 4;
@@ -697,7 +720,8 @@ __device__ __forceinline__ void emb_add_clipped(const T* __restrict__ dY, const 
         float f[4 * Q];
         unpack16(q[u], f, dY);
 #pragma unroll
-        for (int e = 0; e < Q; ++e) acc[e] = fma4(c, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]), acc[e]);
+        for (int e = 0; e < Q; ++e)
+          acc[e] = fma4(c, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]), acc[e]);
       }
     }
     while (longs) {
@@ -717,18 +741,31 @@ __device__ __forceinline__ void emb_add_clipped(const T* __restrict__ dY, const 
 // the chunk's counter (a fixed split left 10% of the SMs' time idle behind the blocks with heavy
 // rows).  ACCUMULATE: rows that occur are added to, the others left alone.
 // NOISE: Box-Muller tables in shared memory; the normals' arithmetic is then what bounds the
-// kernel, the stores of S otherwise.
+// kernel, the stores of S otherwise.  norms null (small calls): every block forms the B norms from
+// the slots itself, which is shorter than another launch, and the first writes norms_out.
 template <typename T, bool NOISE, bool ACCUMULATE>
 __global__ void __launch_bounds__(kEmbThreads, NOISE ? 4 : 3)
-    emb_sum_kernel(const T* __restrict__ dY, EmbIndex ix, int T_len, int V_rows, int d, const float* __restrict__ norms,
-                   float C, float scale, double noise_std, PhiloxKey key, uint32_t layer_id, StepRef step,
-                   float* __restrict__ S) {
+    emb_sum_kernel(const T* __restrict__ dY, EmbIndex ix, int B, int T_len, int V_rows, int d,
+                   const float* __restrict__ norms_in, float* __restrict__ norms_out, float C, float scale,
+                   double noise_std, PhiloxKey key, uint32_t layer_id, StepRef step, float* __restrict__ S) {
   griddep_enter();
   constexpr int Q = kEmbQuads<T>;
   __shared__ float4 part[kEmbWarps][32 * Q];
   __shared__ double2 tab_s[NOISE ? kNoiseSharedEntries : 1];
+  __shared__ float norms_s[kEmbSmallSamples];
   if constexpr (NOISE) stage_noise_tables(tab_s);
+  if (!norms_in) {
+    const long long per = static_cast<long long>(T_len) * ix.chunks;
+    for (int i = threadIdx.x / 32; i < B; i += kEmbWarps) {
+      const float n = emb_norm_by_warp(ix.sq + i * per, per, scale, lane_id());
+      if (lane_id() == 0) {
+        norms_s[i] = n;
+        if (norms_out && blockIdx.x == 0 && blockIdx.y == 0) norms_out[i] = n;
+      }
+    }
+  }
   __syncthreads();
+  const float* const norms = norms_in ? norms_in : norms_s;
   const uint32_t step_lo = NOISE ? step.get() : 0u;
   const int warp = threadIdx.x / 32;
   const uint32_t lane = lane_id();

@@ -10,6 +10,7 @@ struct EmbCall {
   long long N() const { return static_cast<long long>(B) * T; }
   int vec() const { return dt == DP_BF16 ? 8 : 4; }
   int chunks() const { return ceil_div(d, 32 * vec()); }                       // of the sum kernel
+  bool small() const { return B <= kEmbSmallSamples && N() * norm_chunks() <= kEmbSmallSlots; }
   int norm_chunks() const { return ceil_div(d, 32 * vec() * kEmbVecs); }  // of the norm kernel
 };
 
@@ -85,8 +86,8 @@ dim3 emb_grid(int chunks, long long items, int per_sm) {
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(chunks));
 }
 
-dp_status emb_sort(const EmbCall& s, const EmbLayout& L, const EmbIndex& ix, int passes, const void* ids, dp_index it, long long padding,
-                   uint8_t* ws, cudaStream_t stream) {
+dp_status emb_sort(const EmbCall& s, const EmbLayout& L, const EmbIndex& ix, int passes, const void* ids, dp_index it,
+                   long long padding, uint8_t* ws, cudaStream_t stream) {
   EmbSort p{};
   p.ids = ids;
   p.index64 = it == DP_I64 ? 1 : 0;
@@ -134,37 +135,38 @@ dp_status emb_norms(const EmbCall& s, const EmbIndex& ix, float scale, float* no
                     cudaStream_t stream) {
   LaunchScope scope(kKindFinalize, stream);
   DP_LAUNCH("emb_norms_kernel", emb_norms_kernel, s.B, kEmbNormThreads, 0, stream, ix.sq,
-            static_cast<long long>(s.T) * s.norm_chunks(), scale, norms, norms_out);
+            static_cast<long long>(s.T) * s.norm_chunks(), scale, s.small(), norms, norms_out);
   return DP_OK;
 }
 
 template <typename T>
-dp_status emb_sum_as(const EmbCall& s, const EmbIndex& ix, const T* dY, const float* norms, float C, float scale,
-                     bool accumulate, double noise_std, unsigned long long seed, StepRef step, unsigned layer_id,
+dp_status emb_sum_as(const EmbCall& s, const EmbIndex& ix, const T* dY, const float* norms, float* norms_out, float C,
+                     float scale, bool accumulate, double noise_std, unsigned long long seed, StepRef step, unsigned layer_id,
                      float* S, cudaStream_t stream) {
   const PhiloxKey key = philox_key_from_seed(seed);
   LaunchScope scope(kKindEmbSum, stream);
   if (accumulate) {
-    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, true>), emb_grid(s.chunks(), s.V, 8), kEmbThreads, 0, stream, dY, ix,
-              s.T, s.V, s.d, norms, C, scale, 0.0, key, layer_id, step, S);
+    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, true>), emb_grid(s.chunks(), s.V, 8), kEmbThreads, 0, stream,
+              dY, ix, s.B, s.T, s.V, s.d, norms, norms_out, C, scale, 0.0, key, layer_id, step, S);
   } else if (noise_std != 0.0) {
-    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, true, false>), emb_grid(s.chunks(), s.V, 4), kEmbThreads, 0, stream, dY, ix,
-              s.T, s.V, s.d, norms, C, scale, noise_std, key, layer_id, step, S);
+    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, true, false>), emb_grid(s.chunks(), s.V, 4), kEmbThreads, 0, stream,
+              dY, ix, s.B, s.T, s.V, s.d, norms, norms_out, C, scale, noise_std, key, layer_id, step, S);
   } else {
-    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, false>), emb_grid(s.chunks(), s.V, 8), kEmbThreads, 0, stream, dY, ix,
-              s.T, s.V, s.d, norms, C, scale, 0.0, key, layer_id, step, S);
+    DP_LAUNCH("emb_sum_kernel", (emb_sum_kernel<T, false, false>), emb_grid(s.chunks(), s.V, 8), kEmbThreads, 0, stream,
+              dY, ix, s.B, s.T, s.V, s.d, norms, norms_out, C, scale, 0.0, key, layer_id, step, S);
   }
   return DP_OK;
 }
 
-dp_status emb_sum(const EmbCall& s, const EmbIndex& ix, const void* dY, const float* norms, float C, float scale,
-                  bool accumulate, double noise_std, unsigned long long seed, StepRef step, unsigned layer_id, float* S,
+// norms null (small calls): formed from the slots by the kernel, which then writes norms_out.
+dp_status emb_sum(const EmbCall& s, const EmbIndex& ix, const void* dY, const float* norms, float* norms_out, float C,
+                  float scale, bool accumulate, double noise_std, unsigned long long seed, StepRef step, unsigned layer_id, float* S,
                   cudaStream_t stream) {
   if (s.dt == DP_BF16)
-    return emb_sum_as(s, ix, static_cast<const __nv_bfloat16*>(dY), norms, C, scale, accumulate, noise_std, seed, step,
-                      layer_id, S, stream);
-  return emb_sum_as(s, ix, static_cast<const float*>(dY), norms, C, scale, accumulate, noise_std, seed, step, layer_id,
-                    S, stream);
+    return emb_sum_as(s, ix, static_cast<const __nv_bfloat16*>(dY), norms, norms_out, C, scale, accumulate, noise_std, seed,
+                      step, layer_id, S, stream);
+  return emb_sum_as(s, ix, static_cast<const float*>(dY), norms, norms_out, C, scale, accumulate, noise_std, seed, step,
+                    layer_id, S, stream);
 }
 
 // Checks shared by the gradient entry points; fills the layout and the number of sort passes.
@@ -232,8 +234,10 @@ dp_status embedding_step(const void* ids, dp_index it, const void* dY, dp_dtype 
   const double noise_std = (sigma == 0.0f) ? 0.0 : static_cast<double>(sigma) * static_cast<double>(C);
   if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
   if ((st = emb_group_sums(s, ix, dY, true, cs)) != DP_OK) return st;
+  if (s.small())
+    return emb_sum(s, ix, dY, nullptr, norms_out, C, scale, false, noise_std, seed, step, layer_id, G_out, cs);
   if ((st = emb_norms(s, ix, scale, norms, norms_out, cs)) != DP_OK) return st;
-  return emb_sum(s, ix, dY, norms, C, scale, false, noise_std, seed, step, layer_id, G_out, cs);
+  return emb_sum(s, ix, dY, norms, nullptr, C, scale, false, noise_std, seed, step, layer_id, G_out, cs);
 }
 
 }  // namespace
@@ -296,7 +300,7 @@ dp_status dp_embedding_clip_accumulate(const void* ids, dp_index it, const void*
   if ((st = emb_sort(s, L, ix, passes, ids, it, padding_idx, ws, cs)) != DP_OK) return st;
   // The long groups' sums are the norm kernel's; the norms themselves are the caller's.
   if ((st = emb_group_sums(s, ix, dY, false, cs)) != DP_OK) return st;
-  return emb_sum(s, ix, dY, norms, C, scale, true, 0.0, 0, step_value(0), 0, G_sum, cs);
+  return emb_sum(s, ix, dY, norms, nullptr, C, scale, true, 0.0, 0, step_value(0), 0, G_sum, cs);
 }
 
 dp_status dp_embedding_step(const void* ids, dp_index it, const void* dY, dp_dtype dt, int B, int T, int V, int d,

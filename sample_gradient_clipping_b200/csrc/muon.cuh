@@ -247,7 +247,8 @@ __device__ __forceinline__ void ns_apply_block(const NsParams& p, int r0, int co
   for (int e = 0; e < 32; ++e) w[e] = row < p.m && e < cols ? p.W[static_cast<long long>(col + e) * p.m + row] : 0.0f;
 #pragma unroll
   for (int e = 0; e < 32; ++e)
-    if (row < p.m && e < cols) p.W[static_cast<long long>(col + e) * p.m + row] = fmaf(p.keep, w[e], -p.rate * turn[lane][e]);
+    if (row < p.m && e < cols)
+      p.W[static_cast<long long>(col + e) * p.m + row] = fmaf(p.keep, w[e], -p.rate * turn[lane][e]);
 }
 
 // One epilogue warp's 32 x 32 block of A or B, turned through shared memory like X's: `product` gives

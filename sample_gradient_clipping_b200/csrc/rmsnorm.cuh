@@ -296,57 +296,134 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1)
   }
 }
 
-constexpr int kGainThreads = 256;
-
-// per_sample[i][j] = sum over the sample's parts, in part order, and the block's share of n_i^2
-// into sq[i][blockIdx.x].  blockIdx.y: sample.
-__global__ void __launch_bounds__(kGainThreads)
-    rmsnorm_gain_kernel(const float* __restrict__ parts, int nparts, int d, float* __restrict__ per_sample,
-                        float* __restrict__ sq) {
+// per_sample[i][j] = sum over the sample's parts, in part order (fp64).  blockIdx.y: sample.
+constexpr int kPartsThreads = 256;
+__global__ void __launch_bounds__(kPartsThreads)
+    rmsnorm_parts_kernel(const float* __restrict__ parts, int nparts, int d, float* __restrict__ per_sample) {
   griddep_enter();
-  __shared__ float part[kGainThreads / 32];
-  const int j = blockIdx.x * kGainThreads + threadIdx.x;
-  const long long i = blockIdx.y;
+  const int j = blockIdx.x * kPartsThreads + threadIdx.x;
+  if (j >= d) return;
+  const float* p = parts + static_cast<long long>(blockIdx.y) * nparts * d + j;
   double sum = 0.0;
-  if (j < d) {
-    const float* p = parts + i * nparts * d + j;
 #pragma unroll 8
-    for (int k = 0; k < nparts; ++k) sum += static_cast<double>(p[static_cast<long long>(k) * d]);
-    per_sample[i * d + j] = static_cast<float>(sum);
-  }
-  const float f = static_cast<float>(sum);
-  const float ss = warp_sum(f * f);
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = ss;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.0f;
-    for (int w = 0; w < kGainThreads / 32; ++w) s += part[w];
-    sq[i * gridDim.x + blockIdx.x] = s;
-  }
+  for (int k = 0; k < nparts; ++k) sum += static_cast<double>(p[static_cast<long long>(k) * d]);
+  per_sample[static_cast<long long>(blockIdx.y) * d + j] = static_cast<float>(sum);
 }
 
-// norms[i] = sqrt(sum of the sample's `blocks` shares), one warp per sample.
-__global__ void rmsnorm_norms_kernel(const float* __restrict__ sq, int blocks, int B, float* __restrict__ norms) {
+// The end of the backward in one launch, a cluster of 8 blocks that share the columns:
+//   per_sample[i][j] = sum over the sample's parts, in part order;
+//   norms[i] = ||per_sample[i]||, from the blocks' squares through distributed shared memory;
+//   with S: S[j] = sum_i c_i per_sample[i][j] + std z_j.
+// A thread holds four columns; threads left over take other samples beside them.  In place of two
+// launches this takes 3.5 us off the shortest calls.  Eight SMs are too few for many parts (4.8 MB of
+// them: 21 us), so those are summed by rmsnorm_parts_kernel first, and are then one part a sample (`parts`
+// and `per_sample` are then the same array).
+constexpr int kFinishCtas = 8;
+constexpr int kFinishThreads = 512;
+constexpr int kFinishChunk = 256;  // samples at a time
+__global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThreads)
+    rmsnorm_finish_kernel(const float* parts, int nparts, int B, int d, float* per_sample, float* __restrict__ norms,
+                          float C, double noise_std, PhiloxKey key, uint32_t layer_id, StepRef step,
+                          float* __restrict__ S) {
   griddep_enter();
-  const int i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-  if (i >= B) return;
-  const float n2 = warp_norm2_from_partials(sq, blocks, blocks, i, threadIdx.x % 32);
-  if (threadIdx.x % 32 == 0) norms[i] = sqrtf(n2);
+  __shared__ float sq[kFinishChunk][kFinishThreads / 32];
+  __shared__ float total[kFinishChunk];  // of this block's columns, read by the cluster
+  __shared__ float c[kFinishChunk];
+  __shared__ double lanes_s[kFinishThreads][4];
+  const int tid = threadIdx.x;
+  const uint32_t rank = cluster_rank();
+  const int quads = d / 4, per = (quads + kFinishCtas - 1) / kFinishCtas;
+  const int first = static_cast<int>(rank) * per;
+  const int mine = max(0, min(per, quads - first));
+  const int width = min(kFinishThreads, (per + 31) / 32 * 32);  // threads a sample, whole warps (per <= 512)
+  const int lanes = kFinishThreads / width, lane = tid / width, t = tid % width;
+  const bool active = lane < lanes, has = active && t < mine;
+  const long long col = 4ll * (first + t);
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int base = 0; base < B; base += kFinishChunk) {
+    const int count = min(kFinishChunk, B - base);
+    if (active) {
+      for (int s = lane; s < count; s += lanes) {
+        float ss = 0.0f;
+        if (has) {
+          const float* p = parts + static_cast<long long>(base + s) * nparts * d + col;
+          double v[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+          for (int k = 0; k < nparts; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(p + static_cast<long long>(k) * d);
+            v[0] += static_cast<double>(x.x);
+            v[1] += static_cast<double>(x.y);
+            v[2] += static_cast<double>(x.z);
+            v[3] += static_cast<double>(x.w);
+          }
+          const float4 f = make_float4(static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]),
+                                       static_cast<float>(v[3]));
+          *reinterpret_cast<float4*>(per_sample + static_cast<long long>(base + s) * d + col) = f;
+          ss = fmaf(f.x, f.x, fmaf(f.y, f.y, fmaf(f.z, f.z, f.w * f.w)));
+        }
+        ss = warp_sum(ss);
+        if (t % 32 == 0) sq[s][t / 32] = ss;
+      }
+    }
+    __syncthreads();
+    for (int s = tid; s < count; s += kFinishThreads) {
+      float sum = 0.0f;
+      for (int w = 0; w < width / 32; ++w) sum += sq[s][w];
+      total[s] = sum;
+    }
+    __syncwarp();
+    cluster_sync_all();
+    for (int s = tid; s < count; s += kFinishThreads) {
+      double n2 = 0.0;
+#pragma unroll
+      for (uint32_t r = 0; r < kFinishCtas; ++r)
+        n2 += static_cast<double>(__uint_as_float(ld_cluster_u32(smem_addr(&total[s]), r)));
+      const float n = static_cast<float>(sqrt(n2));
+      c[s] = clip_factor(n, C);
+      if (rank == 0 && norms) norms[base + s] = n;
+    }
+    __syncthreads();
+    if (S && has) {
+#pragma unroll 4
+      for (int s = lane; s < count; s += lanes) {  // the thread's own values again
+        const float4 x = *reinterpret_cast<const float4*>(per_sample + static_cast<long long>(base + s) * d + col);
+        const double w = static_cast<double>(c[s]);
+        acc[0] = fma(w, static_cast<double>(x.x), acc[0]);
+        acc[1] = fma(w, static_cast<double>(x.y), acc[1]);
+        acc[2] = fma(w, static_cast<double>(x.z), acc[2]);
+        acc[3] = fma(w, static_cast<double>(x.w), acc[3]);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // the totals were read: they may change, or the block may leave
+  }
+  if (!S) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lanes_s[tid][e] = acc[e];
+  __syncthreads();
+  if (lane != 0 || !has) return;
+  double z[4] = {0.0, 0.0, 0.0, 0.0};
+  if (noise_std != 0.0)
+    normals4(static_cast<uint32_t>(col / 4), layer_id, step.get(), kStreamNoise, key, z, NoiseTablesGlobal{}, noise_std);
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    double sum = 0.0;
+    for (int l = 0; l < lanes; ++l) sum += lanes_s[l * width + t][e];
+    o[e] = static_cast<float>(sum + z[e]);
+  }
+  if (DP_DCHECK(col + 4 <= d, 52u, nullptr)) *reinterpret_cast<float4*>(S + col) = make_float4(o[0], o[1], o[2], o[3]);
 }
 
-// S[j] (+)= sum_i c_i per_sample[i][j] + std z_j, four columns a thread.  The norms are given, or
-// (sq non-null) formed from the shares by each block; block 0 then writes norms_out.
+// S[j] += sum_i c_i per_sample[i][j] for given norms, four columns a thread.
 constexpr int kGainSamples = 1024;  // clip factors held at a time
 constexpr int kGainSumThreads = 128;
 __global__ void __launch_bounds__(kGainSumThreads)
-    rmsnorm_sum_kernel(const float* __restrict__ per_sample, const float* __restrict__ norms,
-                       const float* __restrict__ sq, int sq_blocks, int B, int d, float C, int accumulate,
-                       double noise_std, PhiloxKey key, uint32_t layer_id, StepRef step, float* __restrict__ norms_out,
-                       float* __restrict__ S, uint32_t* __restrict__ status) {
+    rmsnorm_sum_kernel(const float* __restrict__ per_sample, const float* __restrict__ norms, int B, int d, float C,
+                       float* __restrict__ S) {
   griddep_enter();
   __shared__ float c[kGainSamples];
   __shared__ double acc_s[kGainSumThreads][4];
-  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // 32 groups of 4 columns a block; the 4 warps share the samples, in a fixed split.
   const int j = (blockIdx.x * 32 + lane) * 4;
@@ -354,17 +431,7 @@ __global__ void __launch_bounds__(kGainSumThreads)
   for (int base = 0; base < B; base += kGainSamples) {
     const int count = min(kGainSamples, B - base);
     __syncthreads();
-    if (sq) {
-      for (int i = warp; i < count; i += kGainSumThreads / 32) {
-        const float n = sqrtf(warp_norm2_from_partials(sq, sq_blocks, sq_blocks, base + i, lane));
-        if (lane == 0) {
-          c[i] = clip_factor(n, C);
-          if (blockIdx.x == 0 && norms_out) norms_out[base + i] = n;
-        }
-      }
-    } else {
-      for (int i = threadIdx.x; i < count; i += kGainSumThreads) c[i] = clip_factor(norms[base + i], C);
-    }
+    for (int i = threadIdx.x; i < count; i += kGainSumThreads) c[i] = clip_factor(norms[base + i], C);
     __syncthreads();
     if (j < d) {
 #pragma unroll 4
@@ -382,18 +449,15 @@ __global__ void __launch_bounds__(kGainSumThreads)
   for (int e = 0; e < 4; ++e) acc_s[threadIdx.x][e] = a[e];
   __syncthreads();
   if (warp != 0 || j >= d) return;
-  double z[4] = {0.0, 0.0, 0.0, 0.0};
-  if (noise_std != 0.0)
-    normals4(static_cast<uint32_t>(j / 4), layer_id, step.get(), kStreamNoise, key, z, NoiseTablesGlobal{}, noise_std);
-  float4 o = accumulate ? *reinterpret_cast<const float4*>(S + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 o = *reinterpret_cast<const float4*>(S + j);
   float* of = &o.x;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    double s = 0.0;
+    double s = static_cast<double>(of[e]);
     for (int w = 0; w < kGainSumThreads / 32; ++w) s += acc_s[w * 32 + lane][e];
-    of[e] = static_cast<float>(static_cast<double>(of[e]) + s + z[e]);
+    of[e] = static_cast<float>(s);
   }
-  if (DP_DCHECK(j + 4 <= d, 52u, status)) *reinterpret_cast<float4*>(S + j) = o;
+  if (DP_DCHECK(j + 4 <= d, 53u, nullptr)) *reinterpret_cast<float4*>(S + j) = o;
 }
 
 }  // namespace dpclip

@@ -40,15 +40,14 @@ int norm_parts(const NormCall& s) {
 }
 
 struct NormLayout {
-  size_t parts, per_sample, sq, total;
+  size_t parts, per_sample, total;
 };
 
 NormLayout norm_layout(const NormCall& s) {
   NormLayout L;
   L.parts = 256;
   L.per_sample = L.parts + align256(static_cast<size_t>(s.B) * norm_parts(s) * s.d * 4);
-  L.sq = L.per_sample + align256(static_cast<size_t>(s.B) * s.d * 4);
-  L.total = L.sq + align256(static_cast<size_t>(s.B) * ceil_div(s.d, kGainThreads) * 4);
+  L.total = L.per_sample + align256(static_cast<size_t>(s.B) * s.d * 4);
   return L;
 }
 
@@ -132,29 +131,31 @@ dp_status check_norm_backward(const NormCall& s, const void* H, const float* gai
   return ws_bytes < L->total ? DP_ERR_WORKSPACE : DP_OK;
 }
 
-// dh, and every sample's gain gradient with its squared norm's shares.
+// More bytes of parts than this are summed by a launch of their own.
+constexpr long long kFinishPartsBytes = 2 << 20;
+
+// dh, every sample's gain gradient and its norm; with S, the clipped sum and the noise too.
 dp_status norm_backward(const NormCall& s, const NormLayout& L, const void* H, const float* gain, const void* dY,
-                        const void* dres, float eps, void* dX, float* per_sample, uint8_t* ws, cudaStream_t stream) {
+                        const void* dres, float eps, void* dX, float* per_sample, float* norms, float C, double noise_std,
+                        unsigned long long seed, StepRef step, unsigned layer_id, float* S, uint8_t* ws,
+                        cudaStream_t stream) {
   float* parts = reinterpret_cast<float*>(ws + L.parts);
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   const dp_status st =
       s.dt == DP_BF16 ? rmsnorm_backward_as<__nv_bfloat16>(s, H, gain, dY, dres, eps, dX, parts, status, stream)
                       : rmsnorm_backward_as<float>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
   if (st != DP_OK) return st;
-  const dim3 grid(static_cast<unsigned>(ceil_div(s.d, kGainThreads)), static_cast<unsigned>(s.B));
+  int nparts = norm_parts(s);
+  if (nparts > 1 && static_cast<long long>(s.B) * nparts * s.d * 4 > kFinishPartsBytes) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(s.d, kPartsThreads)), static_cast<unsigned>(s.B));
+    LaunchScope scope(kKindRmsNormGain, stream);
+    DP_LAUNCH("rmsnorm_parts_kernel", rmsnorm_parts_kernel, grid, kPartsThreads, 0, stream, parts, nparts, s.d, per_sample);
+    parts = per_sample;
+    nparts = 1;
+  }
   LaunchScope scope(kKindRmsNormGain, stream);
-  DP_LAUNCH("rmsnorm_gain_kernel", rmsnorm_gain_kernel, grid, kGainThreads, 0, stream, parts, norm_parts(s), s.d,
-            per_sample, reinterpret_cast<float*>(ws + L.sq));
-  return DP_OK;
-}
-
-dp_status norm_sum(int B, int d, const float* per_sample, const float* norms, const float* sq, float C, bool accumulate,
-                   double noise_std, unsigned long long seed, StepRef step, unsigned layer_id, float* norms_out,
-                   float* S, uint32_t* status, cudaStream_t stream) {
-  LaunchScope scope(kKindRmsNormGain, stream);
-  DP_LAUNCH("rmsnorm_sum_kernel", rmsnorm_sum_kernel, ceil_div(d, 128), kGainSumThreads, 0, stream, per_sample, norms, sq,
-            ceil_div(d, kGainThreads), B, d, C, accumulate ? 1 : 0, noise_std, philox_key_from_seed(seed), layer_id, step,
-            norms_out, S, status);
+  DP_LAUNCH("rmsnorm_finish_kernel", rmsnorm_finish_kernel, kFinishCtas, kFinishThreads, 0, stream, parts, nparts, s.B,
+            s.d, per_sample, norms, C, noise_std, philox_key_from_seed(seed), layer_id, step, S);
   return DP_OK;
 }
 
@@ -170,11 +171,9 @@ dp_status rmsnorm_step(const void* H, const float* gain, const void* dY, const v
   if (std::isinf(C) && sigma != 0.0f) return DP_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  float* per_sample = reinterpret_cast<float*>(ws + L.per_sample);
-  if ((st = norm_backward(s, L, H, gain, dY, dres, eps, dX, per_sample, ws, cs)) != DP_OK) return st;
   const double noise_std = (sigma == 0.0f) ? 0.0 : static_cast<double>(sigma) * static_cast<double>(C);
-  return norm_sum(B, d, per_sample, nullptr, reinterpret_cast<float*>(ws + L.sq), C, false, noise_std, seed, step,
-                  layer_id, norms_out, G_out, nullptr, cs);
+  return norm_backward(s, L, H, gain, dY, dres, eps, dX, reinterpret_cast<float*>(ws + L.per_sample), norms_out, C,
+                       noise_std, seed, step, layer_id, G_out, ws, cs);
 }
 
 }  // namespace
@@ -213,11 +212,8 @@ dp_status dp_rmsnorm_backward(const void* H, const float* gain, const void* dY, 
   if (!per_sample || !norms || !aligned16(per_sample)) return DP_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if ((st = norm_backward(s, L, H, gain, dY, residual_grad, eps, dX, per_sample, ws, cs)) != DP_OK) return st;
-  LaunchScope scope(kKindFinalize, cs);
-  DP_LAUNCH("rmsnorm_norms_kernel", rmsnorm_norms_kernel, ceil_div(B, 8), 256, 0, cs,
-            reinterpret_cast<float*>(ws + L.sq), ceil_div(d, kGainThreads), B, norms);
-  return DP_OK;
+  return norm_backward(s, L, H, gain, dY, residual_grad, eps, dX, per_sample, norms, INFINITY, 0.0, 0, step_value(0), 0,
+                       nullptr, ws, cs);
 }
 
 dp_status dp_rmsnorm_clip_accumulate(const float* per_sample, const float* norms, int B, int d, float C, float* G_sum,
@@ -225,8 +221,11 @@ dp_status dp_rmsnorm_clip_accumulate(const float* per_sample, const float* norms
   DP_NVTX_RANGE();
   if (!per_sample || !norms || !G_sum || !aligned16(per_sample) || !aligned16(G_sum)) return DP_ERR_INVALID_ARG;
   if (B < 1 || d < 1 || d % 4 || !(C > 0.0f)) return DP_ERR_INVALID_ARG;
-  return norm_sum(B, d, per_sample, norms, nullptr, C, true, 0.0, 0, step_value(0), 0, nullptr, G_sum, nullptr,
-                  static_cast<cudaStream_t>(stream));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  LaunchScope scope(kKindRmsNormGain, cs);
+  DP_LAUNCH("rmsnorm_sum_kernel", rmsnorm_sum_kernel, ceil_div(d, 128), kGainSumThreads, 0, cs, per_sample, norms, B, d, C,
+            G_sum);
+  return DP_OK;
 }
 
 dp_status dp_rmsnorm_step(const void* H, const float* gain, const void* dY, const void* residual_grad, dp_dtype dt,
