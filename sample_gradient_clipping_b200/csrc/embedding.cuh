@@ -487,10 +487,10 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
 }
 
 // ------------------------------------------------------------------------------------- norms
-// A chunk of a row in this kernel: kEmbVecs vectors of 16 bytes a lane.  The kernel is a stream of
-// dY rows and a warp needs bytes in flight: one sorted position a warp, one vector a lane and a
-// barrier between positions took 166 us for 8 x 2048 tokens of 4096 in bf16; this stream takes 40 with
-// two vectors and 42 with four (half the blocks fit), 134 MB at 3.4 TB/s.
+// A chunk of a row in this kernel: kEmbVecs vectors of 16 bytes a lane, four rows of them in flight.  The
+// kernel is a stream of dY rows and a warp needs bytes in flight: one sorted position a warp, one vector
+// a lane and a barrier between positions took 162 us for 8 x 2048 tokens of 4096 in bf16; this stream takes
+// 37 (134 MB at 3.6 TB/s), with two rows in flight 39, with four vectors a lane (half the blocks fit) 42.
 constexpr int kEmbVecs = 2;
 constexpr int kEmbWindow = 16;  // sorted positions whose groups a warp takes
 
@@ -550,12 +550,12 @@ __global__ void __launch_bounds__(kEmbThreads, 4)
       const uint32_t at = base + kEmbWarps * lane;
       const uint32_t tok = at < span.y ? ix.toks[at] : 0u;
       const int rows = static_cast<int>(min((span.y - base + kEmbWarps - 1) / kEmbWarps, 32u));
-      for (int k = 0; k < rows; k += 2) {
-        uint4 q0[kEmbVecs], q1[kEmbVecs];
-        load(q0, __shfl_sync(0xFFFFFFFFu, tok, k), true);
-        load(q1, __shfl_sync(0xFFFFFFFFu, tok, (k + 1) & 31), k + 1 < rows);
-        add(q0);
-        add(q1);
+      for (int k = 0; k < rows; k += 4) {
+        uint4 q[4][kEmbVecs];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load(q[u], __shfl_sync(0xFFFFFFFFu, tok, (k + u) & 31), k + u < rows);  // 0: absent
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add(q[u]);
       }
     }
 #pragma unroll
@@ -605,22 +605,24 @@ __global__ void __launch_bounds__(kEmbThreads, 4)
     const int z = (heads >> kEmbWindow) ? kEmbWindow + __ffs(heads >> kEmbWindow) - 1 : 32;
     clear();
     uint32_t first = 0;
-    for (int k = a; k < z; k += 2) {
-      uint4 q0[kEmbVecs], q1[kEmbVecs];
-      const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, tok, k), t1 = __shfl_sync(0xFFFFFFFFu, tok, (k + 1) & 31);
-      const bool r0 = (rows >> k) & 1u, r1 = k + 1 < z && ((rows >> (k + 1)) & 1u);
-      if (!r0 && !r1) continue;
-      load(q0, t0, r0);
-      load(q1, t1, r1);
+    for (int k = a; k < z; k += 4) {
+      const uint32_t want = (rows >> k) & 15u & (z - k < 4 ? (1u << (z - k)) - 1u : 15u);
+      uint4 q[4][kEmbVecs];
+      uint32_t t[4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 4; ++u) t[u] = __shfl_sync(0xFFFFFFFFu, tok, (k + u) & 31);
+      if (!want) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load(q[u], t[u], (want >> u) & 1u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
         const int at = k + u;
-        if (!(u ? r1 : r0)) continue;
+        if (!((want >> u) & 1u)) continue;
         if ((heads >> at) & 1u) {
-          first = u ? t1 : t0;
+          first = t[u];
           clear();
         }
-        add(u ? q1 : q0);
+        add(q[u]);
         if (at + 1 == z || ((heads >> (at + 1)) & 1u)) {
           const float ss = squares();
           if (lane == 0) ix.sq[static_cast<long long>(first) * chunks + chunk] = ss;
