@@ -390,7 +390,8 @@ dp_status dp_rmsnorm_backward(const void* H, const float* gain, const void* dY, 
                               dp_dtype dt, int B, int T, int d, float eps, void* dX, float* per_sample,
                               float* norms, void* workspace, size_t ws_bytes, void* stream);
 
-/* G_sum[d] += sum_i c_i per_sample[i], c_i = min(1, C / norms[i]), no noise (d a multiple of 4). */
+/* G_sum[d] += sum_i c_i per_sample[i], c_i = min(1, C / norms[i]), no noise (d a multiple of
+ * 4, at most 16384: DP_ERR_UNSUPPORTED above). */
 dp_status dp_rmsnorm_clip_accumulate(const float* per_sample, const float* norms, int B, int d, float C,
                                      float* G_sum, void* stream);
 

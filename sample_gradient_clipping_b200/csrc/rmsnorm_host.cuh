@@ -221,6 +221,7 @@ dp_status dp_rmsnorm_clip_accumulate(const float* per_sample, const float* norms
   DP_NVTX_RANGE();
   if (!per_sample || !norms || !G_sum || !aligned16(per_sample) || !aligned16(G_sum)) return DP_ERR_INVALID_ARG;
   if (B < 1 || d < 1 || d % 4 || !(C > 0.0f)) return DP_ERR_INVALID_ARG;
+  if (d > kNormMaxVecs * 8) return DP_ERR_UNSUPPORTED;  // wider than any row of the backward
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   LaunchScope scope(kKindRmsNormGain, cs);
   DP_LAUNCH("rmsnorm_sum_kernel", rmsnorm_sum_kernel, ceil_div(d, 128), kGainSumThreads, 0, cs, per_sample, norms, B, d, C,

@@ -127,6 +127,7 @@ def test_rmsnorm_pieces_reject_on_host(L):
     for k in (dict(per=None), dict(per=ODD), dict(norms=None), dict(B=0), dict(d=0), dict(d=6), dict(C=0.0), dict(C=math.nan),
               dict(G=None), dict(G=ODD)):
         assert acc(**k) == E, k
+    assert acc(d=16388) == acc(d=2**31 - 4) == U
 
 
 def test_rmsnorm_workspace_size(L):
