@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1)
   griddep_enter();
   if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) *status = 0u;
   const int first = blockIdx.x * per;
-  const int rows = min(T_len, first + per) - first;
+  const int rows = min(per, T_len - first);
   const long long base = (static_cast<long long>(blockIdx.y) * T_len + first) * d;
   auto fetch = [&](int row, int slot) {  // thread 0
     const uint32_t bar = smem_addr(full + slot);

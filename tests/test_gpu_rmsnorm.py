@@ -141,6 +141,25 @@ def test_offsets_past_32_bits():
     assert torch.all((Y[4, -1].abs() - 3.0).abs() <= 2 ** -8 * 3.0) and float(Y[4, -2].abs().max()) == 0.0
 
 
+def test_as_many_rows_as_are_taken():
+    """2^31 - 1 rows of one sample: row numbers next to the end of 32 bits.  (32 GiB a tensor; dY is h.)"""
+    d, T = 8, 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 80 * 2 ** 30:
+        pytest.skip("needs 80 GiB of free device memory")
+    h = torch.ones(1, T, d, dtype=torch.bfloat16, device="cuda")
+    dX = torch.full_like(h, 5.0)
+    gain = torch.arange(1, d + 1, dtype=torch.float32, device="cuda")
+    _, per, n = _lib.dp_rmsnorm_backward(h, gain, h, eps=0.0, dX=dX)
+    # r = 1: dX = gain - its mean, exact in bf16, and every row adds 1 to the gain's gradient, exact in
+    # a part's fp32 sum (under 2^24 rows) and in the fp64 sum of the parts.
+    want = (gain - gain.mean()).to(torch.bfloat16)
+    for rows in (dX[0, :1000], dX[0, T // 2:T // 2 + 1000], dX[0, -1000:]):
+        assert torch.all(rows == want)
+    assert torch.all(dX[0].view(-1, 8)[::4096] == want)
+    assert torch.all(per == float(np.float32(T)))
+    assert abs(float(n) - T * np.sqrt(d)) <= 4 * U32 * T * np.sqrt(d)
+
+
 def test_gradients_against_differences():
     """The backward of the forward that is called, by central differences in fp32."""
     h_h, h, y_h, y, gain_h, gain = _draw(1, 2, 16, "f32", 9, n=2)
