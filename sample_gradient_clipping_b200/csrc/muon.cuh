@@ -421,6 +421,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
+      int issued = 0;
       bool ok = true;
       for (int u = first; ok && u < p.num_units; u += step) {
         const NsUnit w = ns_unit<Cfg>(p, u);
@@ -458,6 +459,16 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
             stage = 0;
             phase ^= 1u;
           }
+          ++issued;
+        }
+      }
+      // No copy may still write shared memory when the CTA leaves (or SPLIT uses it again), not even after
+      // a wait elsewhere ran out.  The pair's copies arrive at the leader, and its peer leaves after it.
+      const unsigned long long t0 = global_timer_ns();
+      for (int k = 0; leader && k < Cfg::STAGES && k < issued; ++k) {
+        stage = stage > 0 ? stage - 1 : Cfg::STAGES - 1;
+        if (stage == Cfg::STAGES - 1) phase ^= 1u;
+        while (!mbar_try_wait(smem_addr(full + stage), phase) && global_timer_ns() - t0 < kWaitLimitNs) {
         }
       }
     }
