@@ -422,8 +422,8 @@ dp_status dp_rmsnorm_step_dev_step(const void* H, const float* gain, const void*
  * two fp16 parts.  Five steps are within 2e-3 of the exact iteration (relative Frobenius error) for
  * gradients with noise in every direction, which privatised ones have; for a matrix of exactly
  * low rank, whose rounding errors grow where it has nothing, within 2e-2.
- *   - Dimensions are multiples of 8, at least 8; rows*cols <= 2^34, the smaller <= 65536;
- *     1 <= steps <= 32.
+ *   - Dimensions are multiples of 8, at least 8; rows*cols <= 2^34, the smaller <= 65536,
+ *     the larger <= 2^30; 1 <= steps <= 32.
  *   - A matrix of zeros gives zeros; infinities or NaN in it give NaN.
  *   - Results are the same bits on every run.  Capture after one ordinary call of the same shape. */
 

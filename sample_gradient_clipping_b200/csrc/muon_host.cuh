@@ -10,6 +10,7 @@ constexpr int kMuonMaxSide = 65536;  // of the smaller dimension: its Gram matri
 bool valid_muon(int rows, int cols) {
   if (rows < 8 || cols < 8 || rows % 8 || cols % 8) return false;
   if (static_cast<long long>(rows) * cols > (1ll << 34)) return false;
+  if (std::max(rows, cols) > (1 << 30)) return false;  // the kernels' column numbers, up to a tile past the end, are 32 bits
   return std::min(rows, cols) <= kMuonMaxSide;
 }
 

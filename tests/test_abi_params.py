@@ -145,7 +145,7 @@ def test_muon_rejects_on_host(L):
 
     for k in (dict(G=None), dict(G=ODD), dict(dt=3), dict(m=0), dict(m=12), dict(n=4), dict(n=36), dict(steps=0),
               dict(steps=33), dict(U=None), dict(U=ODD), dict(U=FAKE), dict(ws=None), dict(ws=FAKE + 16),
-              dict(m=131072, n=131080), dict(m=65544, n=65544)):
+              dict(m=131072, n=131080), dict(m=65544, n=65544), dict(m=8, n=2**30 + 8)):
         assert ortho(**k) == E, k
     assert ortho(n_ws=1000) == W
 
