@@ -317,6 +317,9 @@ dp_status dp_projected_adam_step(float* W, const float* R, float* m, float* v, c
  *   - d is a multiple of 8 (bf16) or 4 (fp32); B*T < 2^31; V*d <= 2^34; scale is finite.
  *   - Results are the same bits on every run.  A row that no token names gets the noise alone
  *     (the noise of a private step covers every row).
+ *   - A table that is the output projection too has a second gradient, that linear's.  Clipped as
+ *     two layers, the two are bounded apart: their sum may be as long as the sum of the two bounds
+ *     (flat clipping: sqrt(2) C), which the noise has to cover.
  *   - A workspace serves one call at a time: calls that may overlap (other streams, graphs replayed
  *     beside each other) each need their own.  So it is for the calls further below. */
 
