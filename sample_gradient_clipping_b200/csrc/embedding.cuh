@@ -492,11 +492,13 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
 // a lane and a barrier between positions took 162 us for 8 x 2048 tokens of 4096 in bf16; this stream takes
 // 37 (134 MB at 3.6 TB/s), with two rows in flight 39, with four vectors a lane (half the blocks fit) 42.
 constexpr int kEmbVecs = 2;
-constexpr int kEmbWindow = 16;  // sorted positions whose groups a warp takes
+// Sorted positions whose groups a warp takes.  Fewer spread short calls over more warps (4 x 16 tokens of 64:
+// 9.5 us with 16, 7.2 with 4; 16496 of 1032: 18.6 and 16.9; 16384 of 4096: 40 both; with 8: 7.5, 16.3 and 42).
+constexpr int kEmbWindow = 4;
 
 // blockIdx.y: chunk.  Long groups first, each by a block whose warps share its rows (all there is to do
 // when the norms are given: `short_groups` false).  Then each warp
-// takes the short groups that start among 16 positions: these end within 32, so one load of the
+// takes the short groups that start among kEmbWindow positions: these end within 32, so one load of the
 // order shows them all, and their rows are added as one stream, cut where a group ends.
 template <typename T>
 __global__ void __launch_bounds__(kEmbThreads, 4)
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(kEmbThreads, 4)
     const bool row = in && (use & kEmbUseMask) == kEmbRow && ix.keys[p] != none;
     const uint32_t heads = __ballot_sync(0xFFFFFFFFu, (use & kEmbHead) != 0);
     const uint32_t rows = __ballot_sync(0xFFFFFFFFu, row);
-    if (!(heads & 0xFFFFu)) continue;
+    if (!(heads & ((1u << kEmbWindow) - 1u))) continue;
     const int a = __ffs(heads) - 1;
     const int z = (heads >> kEmbWindow) ? kEmbWindow + __ffs(heads >> kEmbWindow) - 1 : 32;
     clear();
