@@ -8,6 +8,7 @@ other code.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -542,7 +543,7 @@ def dp_embedding_lookup(W, ids, scale=1.0, out=None, out_dtype=None, stream=None
 
     if W.dim() != 2:
         raise ValueError("W must be [V, d]")
-    V, d = int(W.shape[0]), int(W.shape[1])
+    V, d = W.shape
     dtype = out.dtype if out is not None else (out_dtype or W.dtype)
     shape = (*ids.shape, d)
     _expect(out, "out", shape, dtype)
@@ -556,11 +557,15 @@ def dp_embedding_lookup(W, ids, scale=1.0, out=None, out_dtype=None, stream=None
 
 
 def _embedding_dims(ids, dY):
-    if ids.dim() != 2 or dY.dim() != 3 or tuple(dY.shape[:2]) != tuple(ids.shape):
-        raise ValueError("ids must be [B, T] and dY [B, T, d]")
-    return int(dY.shape[0]), int(dY.shape[1]), int(dY.shape[2])
+    if dY.dim() == 3:
+        B, T, d = dY.shape
+        if ids.shape == (B, T):
+            return B, T, d
+    raise ValueError("ids must be [B, T] and dY [B, T, d]")
 
 
+# The sizes depend on their arguments alone, and a call through ctypes costs a microsecond.
+@functools.lru_cache(maxsize=1024)
 def embedding_workspace_size(B, T, V, d, dtype_code=DP_BF16):
     return int(lib().dp_embedding_workspace_size(B, T, V, d, dtype_code))
 
@@ -640,11 +645,12 @@ def dp_rmsnorm(X, gain, eps=1e-6, residual=None, H_out=None, Y=None, stream=None
     """(y, h): h = X + residual (X itself without one), y = h / rms(h) * gain, over the last axis."""
     import torch
 
-    d = int(X.shape[-1])
+    shape, dtype = X.shape, X.dtype
+    d = shape[-1]
     _expect(gain, "gain", (d,), torch.float32)
-    _expect(residual, "residual", X.shape, X.dtype)
-    _expect(H_out, "H_out", X.shape, X.dtype)
-    _expect(Y, "Y", X.shape, X.dtype)
+    _expect(residual, "residual", shape, dtype)
+    _expect(H_out, "H_out", shape, dtype)
+    _expect(Y, "Y", shape, dtype)
     if residual is None and H_out is not None:
         raise ValueError("H_out needs a residual: without one h is X itself")
     with _Launch(stream, "X gain residual H_out Y", X, gain, residual, H_out, Y) as s:
@@ -658,6 +664,7 @@ def dp_rmsnorm(X, gain, eps=1e-6, residual=None, H_out=None, Y=None, stream=None
     return Y, H
 
 
+@functools.lru_cache(maxsize=1024)
 def rmsnorm_workspace_size(B, T, d, dtype_code=DP_BF16):
     return int(lib().dp_rmsnorm_workspace_size(B, T, d, dtype_code))
 
@@ -665,14 +672,15 @@ def rmsnorm_workspace_size(B, T, d, dtype_code=DP_BF16):
 def _norm_dims(H, dY, gain, residual_grad, dX):
     import torch
 
-    if H.dim() != 3:
+    shape, dtype = H.shape, H.dtype
+    if len(shape) != 3:
         raise ValueError("H must be [B, T, d]")
-    d = int(H.shape[2])
-    _expect(dY, "dY", H.shape, H.dtype)
+    B, T, d = shape
+    _expect(dY, "dY", shape, dtype)
     _expect(gain, "gain", (d,), torch.float32)
-    _expect(residual_grad, "residual_grad", H.shape, H.dtype)
-    _expect(dX, "dX", H.shape, H.dtype)
-    return int(H.shape[0]), int(H.shape[1]), d
+    _expect(residual_grad, "residual_grad", shape, dtype)
+    _expect(dX, "dX", shape, dtype)
+    return B, T, d
 
 
 def dp_rmsnorm_backward(H, gain, dY, eps=1e-6, residual_grad=None, dX=None, per_sample=None, norms=None,
@@ -744,6 +752,7 @@ def dp_rmsnorm_step(H, gain, dY, C, sigma, seed, step, layer_id, eps=1e-6, resid
     return dX, G_out, norms_out
 
 
+@functools.lru_cache(maxsize=1024)
 def muon_workspace_size(rows, cols):
     return int(lib().dp_muon_workspace_size(rows, cols))
 
