@@ -34,7 +34,6 @@ constexpr uint32_t kStatusIdRange = 900u;
 
 constexpr int kEmbSortThreads = 1024;
 constexpr int kEmbSortWarps = kEmbSortThreads / 32;
-constexpr int kEmbRadix = 256;
 // A group of more tokens than this is summed by a whole block, and its sum kept: the last kernel
 // then reads 4 bytes an element once instead of its rows (2 bytes each in bf16).
 constexpr int kEmbLongGroup = 16;
@@ -315,7 +314,7 @@ struct EmbSort {
   long long N;
   int V;
   long long padding;
-  int passes;            // of 8 bits
+  int passes;            // of BITS bits
   uint32_t* keys[2];     // ping-pong: pass p writes [p & 1]
   uint32_t* toks[2];
   EmbIndex ix;           // its counters and rows are cleared here; CTAS = 1 fills the rest
@@ -324,25 +323,31 @@ struct EmbSort {
   uint32_t* status;
 };
 
-// Sorts the N tokens by key in stable passes of 8 bits.  One cluster: every warp owns a contiguous
+// Sorts the N tokens by key in stable passes of BITS bits: 8, or 9 where that is a pass less (V of 256 ..
+// 511, 2^16 .. 2^18 - 1, from 2^24).  One cluster: every warp owns a contiguous
 // range of positions, in (block, warp) order, so the position of its next token of a digit is
 // (digits below) + (blocks before) + (warps before) + (its own so far), and blocks exchange only
-// their 256 digit totals, through distributed shared memory.  All of this is latency, which one
+// their digit totals, through distributed shared memory.  All of this is latency, which one
 // launch keeps smallest: with the keys of a pass held in registers, 8 blocks take about 5 us a pass
 // at 16384 tokens.  CTAS = 1 serves calls of a few thousand tokens, where a cluster's barriers would
 // cost more than its blocks save.
-template <int CTAS>
+template <int BITS>
+constexpr size_t kEmbSortSmem = sizeof(uint32_t) * (kEmbSortWarps << BITS);
+template <int CTAS, int BITS>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 1)
     emb_sort_kernel(const __grid_constant__ EmbSort p) {
   griddep_enter();
-  __shared__ uint32_t hist[kEmbSortWarps][kEmbRadix];  // counts, then each warp's next position per digit
-  __shared__ uint32_t quarter[4][kEmbRadix];           // totals of 8 warps each
-  __shared__ uint32_t total[kEmbRadix];                // this block's digit totals, read by the cluster
-  __shared__ uint32_t base[kEmbRadix];
+  constexpr int kRadix = 1 << BITS;
+  constexpr int kParts = kEmbSortThreads / kRadix, kPartWarps = kEmbSortWarps / kParts;
+  extern __shared__ uint32_t hist_raw[];
+  auto const hist = reinterpret_cast<uint32_t(*)[kRadix]>(hist_raw);  // [warp]: counts, then its next position per digit
+  __shared__ uint32_t part_total[kParts][kRadix];  // of kPartWarps warps each
+  __shared__ uint32_t total[kRadix];               // this block's digit totals, read by the cluster
+  __shared__ uint32_t base[kRadix];
   const int tid = threadIdx.x, warp = tid / 32;
   const uint32_t lane = lane_id();
   const uint32_t rank = CTAS > 1 ? cluster_rank() : 0u;
-  const int digit = tid % kEmbRadix, part = tid / kEmbRadix;
+  const int digit = tid % kRadix, part = tid / kRadix;
   const uint32_t below = (1u << lane) - 1u;
   auto sync_all = [] {
     if constexpr (CTAS > 1) {
@@ -371,7 +376,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
   sync_all();  // the status word is cleared before a key may set it
 
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = 8 * pass;
+    const int shift = BITS * pass;
     const uint32_t* kin = (pass & 1) ? p.keys[0] : p.keys[1];
     const uint32_t* tin = (pass & 1) ? p.toks[0] : p.toks[1];
     uint32_t* kout = (pass & 1) ? p.keys[1] : p.keys[0];
@@ -389,29 +394,34 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
         ht[i] = at < end ? tok_at(at) : 0u;
       }
     }
-    for (int q = tid; q < kEmbSortWarps * kEmbRadix; q += kEmbSortThreads) (&hist[0][0])[q] = 0u;
+    for (int q = tid; q < kEmbSortWarps * kRadix; q += kEmbSortThreads) hist_raw[q] = 0u;
     __syncthreads();
     if (held) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        if (begin + 32 * i + lane < end) atomicAdd(&hist[warp][(hk[i] >> shift) & (kEmbRadix - 1)], 1u);
+        if (begin + 32 * i + lane < end) atomicAdd(&hist[warp][(hk[i] >> shift) & (kRadix - 1)], 1u);
     } else {
       for (long long at = begin + lane; at < end; at += 32)
-        atomicAdd(&hist[warp][(key_at(at) >> shift) & (kEmbRadix - 1)], 1u);
+        atomicAdd(&hist[warp][(key_at(at) >> shift) & (kRadix - 1)], 1u);
     }
     __syncthreads();
-    {  // warps before this one, among the 8 of its quarter
+    {  // warps before this one, among those of its part
       uint32_t sum = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const uint32_t c = hist[8 * part + w][digit];
-        hist[8 * part + w][digit] = sum;
+      for (int w = 0; w < kPartWarps; ++w) {
+        const uint32_t c = hist[kPartWarps * part + w][digit];
+        hist[kPartWarps * part + w][digit] = sum;
         sum += c;
       }
-      quarter[part][digit] = sum;
+      part_total[part][digit] = sum;
     }
     __syncthreads();
-    if (part == 0) total[digit] = quarter[0][digit] + quarter[1][digit] + quarter[2][digit] + quarter[3][digit];
+    if (part == 0) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) sum += part_total[q][digit];
+      total[digit] = sum;
+    }
     sync_all();
     uint32_t before = 0;
     if (part == 0) {
@@ -429,12 +439,13 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
       base[digit] = all;
     }
     __syncthreads();
-    if (warp == 0) {  // exclusive sum of the 256 digit totals, 8 digits a lane
-      uint32_t c[8], sum = 0;
+    if (warp == 0) {  // exclusive sum of the digit totals, kPer digits a lane
+      constexpr int kPer = kRadix / 32;
+      uint32_t c[kPer], sum = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < kPer; ++e) {
         c[e] = sum;
-        sum += base[8 * lane + e];
+        sum += base[kPer * lane + e];
       }
       uint32_t run = sum;
 #pragma unroll
@@ -443,20 +454,20 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
         if (lane >= static_cast<uint32_t>(o)) run += x;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) base[8 * lane + e] = run - sum + c[e];
+      for (int e = 0; e < kPer; ++e) base[kPer * lane + e] = run - sum + c[e];
     }
     __syncthreads();
     if (part == 0) base[digit] += before;
     __syncthreads();
     {
       uint32_t b = base[digit];
-      for (int q = 0; q < part; ++q) b += quarter[q][digit];
+      for (int q = 0; q < part; ++q) b += part_total[q][digit];
 #pragma unroll
-      for (int w = 0; w < 8; ++w) hist[8 * part + w][digit] += b;
+      for (int w = 0; w < kPartWarps; ++w) hist[kPartWarps * part + w][digit] += b;
     }
     __syncthreads();
     auto place = [&](bool ok, uint32_t key, uint32_t tok) {
-      const uint32_t dg = ok ? (key >> shift) & (kEmbRadix - 1) : kEmbRadix;  // a lane without a token: no digit
+      const uint32_t dg = ok ? (key >> shift) & (kRadix - 1) : kRadix;  // a lane without a token: no digit
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
       uint32_t pos = 0;
       if (ok) pos = hist[warp][dg] + __popc(same & below);

@@ -86,6 +86,31 @@ dim3 emb_grid(int chunks, long long items, int per_sm) {
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(chunks));
 }
 
+// The stable passes of `bits` bits that order keys 0 .. V, V itself being the key of a token without a group.
+int emb_passes(int V, int bits) {
+  int passes = 1;
+  while ((static_cast<unsigned long long>(V) >> (bits * passes)) != 0) ++passes;
+  return passes;
+}
+int emb_digit_bits(int V) { return emb_passes(V, 9) < emb_passes(V, 8) ? 9 : 8; }
+
+template <int CTAS, int BITS>
+dp_status emb_sort_launch(const EmbSort& p, cudaStream_t stream) {
+  if constexpr (BITS > 8) {  // past 48 KB with the static arrays
+    static std::atomic<bool> configured[64] = {};
+    int dev = 0;
+    DP_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+      DP_CUDA(cudaFuncSetAttribute(emb_sort_kernel<CTAS, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(kEmbSortSmem<BITS>)));
+      if (dev >= 0 && dev < 64) configured[dev].store(true);
+    }
+  }
+  LaunchScope scope(kKindEmbSort, stream);
+  DP_LAUNCH("emb_sort_kernel", (emb_sort_kernel<CTAS, BITS>), CTAS, kEmbSortThreads, kEmbSortSmem<BITS>, stream, p);
+  return DP_OK;
+}
+
 dp_status emb_sort(const EmbCall& s, const EmbLayout& L, const EmbIndex& ix, int passes, const void* ids, dp_index it,
                    long long padding, uint8_t* ws, cudaStream_t stream) {
   EmbSort p{};
@@ -103,15 +128,10 @@ dp_status emb_sort(const EmbCall& s, const EmbLayout& L, const EmbIndex& ix, int
   p.turns = s.chunks();
   p.T = s.T;
   p.status = reinterpret_cast<uint32_t*>(ws);
-  if (p.N <= kEmbSortAlone) {
-    LaunchScope scope(kKindEmbSort, stream);
-    DP_LAUNCH("emb_sort_kernel", emb_sort_kernel<1>, 1, kEmbSortThreads, 0, stream, p);
-    return DP_OK;
-  }
-  {
-    LaunchScope scope(kKindEmbSort, stream);
-    DP_LAUNCH("emb_sort_kernel", emb_sort_kernel<8>, 8, kEmbSortThreads, 0, stream, p);
-  }
+  const bool wide = emb_digit_bits(s.V) == 9;
+  if (p.N <= kEmbSortAlone) return wide ? emb_sort_launch<1, 9>(p, stream) : emb_sort_launch<1, 8>(p, stream);
+  const dp_status st = wide ? emb_sort_launch<8, 9>(p, stream) : emb_sort_launch<8, 8>(p, stream);
+  if (st != DP_OK) return st;
   LaunchScope scope(kKindEmbSort, stream);
   DP_LAUNCH("emb_mark_kernel", emb_mark_kernel, stream_grid(static_cast<unsigned long long>(p.N), 128), 128, 0, stream, ix,
             p.N, s.T, s.V);
@@ -178,9 +198,7 @@ dp_status emb_check(const EmbCall& s, const void* ids, dp_index it, const void* 
   if (!valid_embedding(s) || !std::isfinite(scale)) return DP_ERR_INVALID_ARG;
   *L = emb_layout(s);
   if (ws_bytes < L->total) return DP_ERR_WORKSPACE;
-  // Keys are 0 .. V, V itself being the key of a token without a group.
-  *passes = 1;
-  while (*passes < 4 && (static_cast<unsigned long long>(s.V) >> (8 * *passes)) != 0) ++*passes;
+  *passes = emb_passes(s.V, emb_digit_bits(s.V));
   return DP_OK;
 }
 

@@ -89,6 +89,15 @@ def test_step_matches_the_oracle(shape, dt):
            index="int32" if d % 16 else "int64")
 
 
+@pytest.mark.parametrize("V", [511, 512, 2 ** 18 - 1, 2 ** 18])
+@pytest.mark.parametrize("B,T", [(2, 300), (2, 2500)])
+def test_tables_at_the_ends_of_the_sorts_digits(V, B, T):
+    """Where the digits' width or number changes; uniform ids, the first and last ones among them."""
+    ids = np.random.default_rng(V + T).integers(0, V, (B, T))
+    ids[0, :4] = ids[-1, -4:] = (V - 1, 0, 255, 256)
+    _check(B, T, V, 8, "bf16", seed=V, ids=lambda _: ids, padding_idx=256)
+
+
 @pytest.mark.parametrize("first", [0, 5, 17, 31])
 def test_group_and_row_lengths_around_the_thresholds(first):
     """Groups of 1 to 130 tokens of one id, alone and as rows of several samples, at every phase of the
