@@ -296,18 +296,36 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1)
   }
 }
 
-// per_sample[i][j] = sum over the sample's parts, in part order (fp64).  blockIdx.y: sample.
-constexpr int kPartsThreads = 256;
-__global__ void __launch_bounds__(kPartsThreads)
+// per_sample[i][j] = sum over the sample's parts in fp64, blockIdx.y: sample.  Its 4 to 16 warps take the
+// parts of 128 columns in turn, four columns a lane, and their sums are added in their order.  One thread a
+// column, its parts in a row, made the step of 2048 rows of 768 (1024 parts) 58 us; this makes it 17 to 19.
+constexpr int kPartsWarps = 16;  // at most
+__global__ void __launch_bounds__(kPartsWarps * 32)
     rmsnorm_parts_kernel(const float* __restrict__ parts, int nparts, int d, float* __restrict__ per_sample) {
   griddep_enter();
-  const int j = blockIdx.x * kPartsThreads + threadIdx.x;
-  if (j >= d) return;
-  const float* p = parts + static_cast<long long>(blockIdx.y) * nparts * d + j;
-  double sum = 0.0;
+  __shared__ double sums[kPartsWarps][128];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32, first = blockIdx.x * 128;
+  const int j = first + 4 * lane;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
+  if (j < d) {
+    const float* p = parts + static_cast<long long>(blockIdx.y) * nparts * d + j;
 #pragma unroll 8
-  for (int k = 0; k < nparts; ++k) sum += static_cast<double>(p[static_cast<long long>(k) * d]);
-  per_sample[static_cast<long long>(blockIdx.y) * d + j] = static_cast<float>(sum);
+    for (int k = warp; k < nparts; k += warps) {
+      const float4 x = *reinterpret_cast<const float4*>(p + static_cast<long long>(k) * d);
+      v[0] += static_cast<double>(x.x);
+      v[1] += static_cast<double>(x.y);
+      v[2] += static_cast<double>(x.z);
+      v[3] += static_cast<double>(x.w);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sums[warp][4 * lane + e] = v[e];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= 128 || first + c >= d) return;
+  double sum = 0.0;
+  for (int w = 0; w < warps; ++w) sum += sums[w][c];
+  per_sample[static_cast<long long>(blockIdx.y) * d + first + c] = static_cast<float>(sum);
 }
 
 // The end of the backward in one launch, a cluster of 8 blocks that share the columns:
@@ -315,8 +333,8 @@ __global__ void __launch_bounds__(kPartsThreads)
 //   norms[i] = ||per_sample[i]||, from the blocks' squares through distributed shared memory;
 //   with S: S[j] = sum_i c_i per_sample[i][j] + std z_j.
 // A thread holds four columns; threads left over take other samples beside them.  In place of two
-// launches this takes 3.5 us off the shortest calls.  Eight SMs are too few for many parts (4.8 MB of
-// them: 21 us), so those are summed by rmsnorm_parts_kernel first, and are then one part a sample (`parts`
+// launches this takes 3.5 us off the shortest calls.  Eight SMs are too few for many parts (2 x 486 rows of
+// 396, a part each: 65 us a step, 14 with the launch before), so those are summed by rmsnorm_parts_kernel first, and are then one part a sample (`parts`
 // and `per_sample` are then the same array).
 constexpr int kFinishCtas = 8;
 constexpr int kFinishThreads = 512;

@@ -131,8 +131,11 @@ dp_status check_norm_backward(const NormCall& s, const void* H, const float* gai
   return ws_bytes < L->total ? DP_ERR_WORKSPACE : DP_OK;
 }
 
-// More bytes of parts than this are summed by a launch of their own.
-constexpr long long kFinishPartsBytes = 2 << 20;
+// More parts of a sample, or bytes of them, than these are summed by a launch of their own.  It costs 1 us on
+// the GPU and 2 on the host; up to 16 parts the finish takes as long without it (4 x 16 rows of 256: 8.2 us
+// and 8.0; 16 rows of 4096: 9.2 and 8.9; 2 x 64 of 1024, 64 parts: 18.1 and 9.7).
+constexpr int kFinishParts = 16;
+constexpr long long kFinishPartsBytes = 512 << 10;
 
 // dh, every sample's gain gradient and its norm; with S, the clipped sum and the noise too.
 dp_status norm_backward(const NormCall& s, const NormLayout& L, const void* H, const float* gain, const void* dY,
@@ -146,10 +149,11 @@ dp_status norm_backward(const NormCall& s, const NormLayout& L, const void* H, c
                       : rmsnorm_backward_as<float>(s, H, gain, dY, dres, eps, dX, parts, status, stream);
   if (st != DP_OK) return st;
   int nparts = norm_parts(s);
-  if (nparts > 1 && static_cast<long long>(s.B) * nparts * s.d * 4 > kFinishPartsBytes) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(s.d, kPartsThreads)), static_cast<unsigned>(s.B));
+  if (nparts > kFinishParts || (nparts > 1 && static_cast<long long>(s.B) * nparts * s.d * 4 > kFinishPartsBytes)) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(s.d, 128)), static_cast<unsigned>(s.B));
+    const int warps = nparts <= 8 ? 4 : nparts <= 32 ? 8 : kPartsWarps;  // two to four parts a warp, or more
     LaunchScope scope(kKindRmsNormGain, stream);
-    DP_LAUNCH("rmsnorm_parts_kernel", rmsnorm_parts_kernel, grid, kPartsThreads, 0, stream, parts, nparts, s.d, per_sample);
+    DP_LAUNCH("rmsnorm_parts_kernel", rmsnorm_parts_kernel, grid, 32 * warps, 0, stream, parts, nparts, s.d, per_sample);
     parts = per_sample;
     nparts = 1;
   }
