@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kEmbThreads, 4)
 __device__ __forceinline__ float emb_norm_by_warp(const float* __restrict__ slots, long long count, float scale,
                                                   uint32_t lane) {
   double acc = 0.0;
-#pragma unroll 4
+#pragma unroll 8
   for (long long k = lane; k < count; k += 32) acc += static_cast<double>(slots[k]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
@@ -658,9 +658,9 @@ __device__ __forceinline__ float emb_norm_by_warp(const float* __restrict__ slot
 
 // norms[i] = |scale| sqrt(sum of the sample's T * chunks slots): one block a sample, in a fixed order.
 // `by_warp`: in the order above, by one warp, which is what the sum kernel does for itself in small
-// calls (kEmbSmallSlots), so that every entry point gives a shape's norms in the same bits.
+// calls (kEmbSmallReads), so that every entry point gives a shape's norms in the same bits.
 constexpr int kEmbNormThreads = 512;
-constexpr long long kEmbSmallSlots = 8192;
+constexpr long long kEmbSmallReads = 4;
 constexpr int kEmbSmallSamples = 64;
 __global__ void __launch_bounds__(kEmbNormThreads)
     emb_norms_kernel(const float* __restrict__ sq, long long per_sample, float scale, bool by_warp,
@@ -832,12 +832,13 @@ __global__ void __launch_bounds__(kEmbThreads, NOISE ? 4 : 3)
     }
     __syncthreads();
   }
-  // A turn is up to 8 rows, `turns` apart: ids near each other are often alike in frequency (common
+  // A turn is a few rows, `turns` apart: ids near each other are often alike in frequency (common
   // ones first), and a warp that took 8 neighbours would have all the long rows.
   const long long warps = static_cast<long long>(gridDim.x) * kEmbWarps;
-  // At least two turns a warp; fewer rows a turn would queue on the counter (50257 turns took 100 us).
+  // Up to 8 rows, and two turns a warp; but at most 8192 turns where that leaves less than 8, since they queue on
+  // the counter at about one a nanosecond (512 tokens of 64, V = 32000, a row a turn: 49 us a step, now 33).
   const long long share = V_rows / (2 * warps);
-  const int count = share < 1 ? 1 : share > 8 ? 8 : static_cast<int>(share);
+  const int count = share >= 8 ? 8 : max(static_cast<int>(share), (V_rows + 8191) / 8192);  // below 32
   const long long turns = (V_rows + count - 1) / count;
   for (;;) {
     uint32_t turn = lane == 0 ? atomicAdd(ix.turns + blockIdx.y, 1u) : 0u;

@@ -10,7 +10,11 @@ struct EmbCall {
   long long N() const { return static_cast<long long>(B) * T; }
   int vec() const { return dt == DP_BF16 ? 8 : 4; }
   int chunks() const { return ceil_div(d, 32 * vec()); }                       // of the sum kernel
-  bool small() const { return B <= kEmbSmallSamples && N() * norm_chunks() <= kEmbSmallSlots; }
+  // Reads that follow one another where a block's 8 warps form all norms, 8 of 32 slots at a time.
+  bool small() const {
+    const long long each = (static_cast<long long>(T) * norm_chunks() + 255) / 256;
+    return B <= kEmbSmallSamples && ceil_div(B, kEmbWarps) * each <= kEmbSmallReads;
+  }
   int norm_chunks() const { return ceil_div(d, 32 * vec() * kEmbVecs); }  // of the norm kernel
 };
 
@@ -75,8 +79,9 @@ EmbIndex emb_index(const EmbCall& s, const EmbLayout& L, uint8_t* ws, int passes
   return ix;
 }
 
-// Up to this many tokens one block sorts them.
-constexpr long long kEmbSortAlone = 4096;
+// Up to this many tokens one block sorts them and marks the order (512 tokens: 18.7 us a step against 20.1 with
+// a cluster and the marks' own launch; 1024: 22.7 and 23.5; 2048: 28.0 and 25.4; 4096: 38 and 29).
+constexpr long long kEmbSortAlone = 1024;
 
 // Grid of the norm and sum kernels: x over warps' items, y over chunks, `per_sm` blocks an SM.
 dim3 emb_grid(int chunks, long long items, int per_sm) {
