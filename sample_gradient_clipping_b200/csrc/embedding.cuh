@@ -329,7 +329,7 @@ struct EmbSort {
 // (digits below) + (blocks before) + (warps before) + (its own so far), and blocks exchange only
 // their digit totals, through distributed shared memory.  All of this is latency, which one
 // launch keeps smallest: with the keys of a pass held in registers, 8 blocks take about 5 us a pass
-// at 16384 tokens.  CTAS = 1 serves calls of a few thousand tokens, where a cluster's barriers would
+// at 16384 tokens.  CTAS = 1 serves calls of up to a thousand tokens, where a cluster's barriers would
 // cost more than its blocks save.
 template <int BITS>
 constexpr size_t kEmbSortSmem = sizeof(uint32_t) * (kEmbSortWarps << BITS);

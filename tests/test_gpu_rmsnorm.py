@@ -114,6 +114,25 @@ def test_step(dt, d, B, T, sigma):
         assert np.all(np.abs(host(S) - 1.0 - ref["S"]) <= bS + U32 * (1.0 + np.abs(ref["S"])))
 
 
+@pytest.mark.parametrize("B,T,d,dt", [
+    # parts of a sample: 7, 2 and 4 of many bytes, 32, 37, one a row, and more than a row each
+    (300, 20, 256, "bf16"), (64, 2, 2056, "bf16"), (32, 4, 4096, "bf16"), (16, 32, 2048, "bf16"), (64, 40, 128, "bf16"),
+    (2, 486, 396, "f32"), (1, 700, 132, "f32"), (1, 2500, 64, "f32"),
+])
+def test_parts_of_a_sample(B, T, d, dt):
+    h_h, h, y_h, y, gain_h, gain = _draw(B, T, d, dt, B + T + d, n=2)
+    C = 0.8
+    ref = oracle.rmsnorm_step(h_h, gain_h, y_h, float(np.float32(C)), 0.0, 0, 0, 0, float(np.float32(EPS)))
+    dX, G, n = _lib.dp_rmsnorm_step(h, gain, y, C, 0.0, 0, 0, 0, eps=EPS)
+    bX, bper, bn, bS = _bounds(h_h, gain_h, y_h, ref, C, dt, T, d, None)
+    assert np.all(np.abs(host(dX) - ref["dX"]) <= bX + 1e-30)
+    assert np.all(np.abs(host(n) - ref["norms"]) <= bn + 1e-30)
+    # (the samples' terms are added in fp64, so more of them add no rounding)
+    assert np.all(np.abs(host(G) - ref["out"]) <= bS)
+    _, per, n2 = _lib.dp_rmsnorm_backward(h, gain, y, eps=EPS)
+    assert torch.equal(n, n2) and np.all(np.abs(host(per) - ref["per_sample"]) <= bper + 1e-30)
+
+
 def test_many_samples():
     h_h, h, y_h, y, gain_h, gain = _draw(2500, 3, 40, "f32", 8, n=2)
     ref = oracle.rmsnorm_step(h_h, gain_h, y_h, 0.5, 0.0, 0, 0, 0, float(np.float32(EPS)))
