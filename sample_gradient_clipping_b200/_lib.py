@@ -223,6 +223,23 @@ def _bt_dims(X, dY):
     return int(X.shape[0]), int(X.shape[1]), int(X.shape[2]), int(dY.shape[2])
 
 
+def _holds_fp32(t, name, count):
+    """The library writes or reads ``count`` fp32 values at t's pointer."""
+    import torch
+
+    if t is not None and (t.dtype != torch.float32 or t.numel() < count or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {torch.float32} of {count} elements, got {t.dtype} {list(t.shape)}")
+
+
+def _projection_width(P, X, d_out):
+    """r of a projection P [d_out, r] in X's dtype, 0 without one."""
+    if P is None:
+        return 0
+    if P.dim() != 2 or P.shape[0] != d_out or P.dtype != X.dtype or not P.is_contiguous():
+        raise ValueError(f"P must be contiguous {X.dtype} of shape [{d_out}, r], got {P.dtype} {list(P.shape)}")
+    return int(P.shape[1])
+
+
 def workspace_size(B, T, d_in, d_out, r=0, dtype_code=DP_BF16, method="auto"):
     return int(lib().dp_workspace_size_for(B, T, d_in, d_out, r, dtype_code, METHODS[method]))
 
@@ -244,7 +261,8 @@ def dp_per_sample_norms(X, dY, P=None, method="auto", norms=None, workspace=None
     import torch
 
     B, T, d_in, d_out = _bt_dims(X, dY)
-    r = int(P.shape[1]) if P is not None else 0
+    r = _projection_width(P, X, d_out)
+    _holds_fp32(norms, "norms", B)
     ws = _workspace(X, dY, r, workspace)
     if norms is None:
         norms = torch.empty(B, dtype=torch.float32, device=X.device)
@@ -257,7 +275,9 @@ def dp_per_sample_norms(X, dY, P=None, method="auto", norms=None, workspace=None
 def dp_clip_accumulate(X, dY, norms, C, G_sum, P=None, workspace=None, stream=None):
     """G_sum += sum_i c_i X_i^T dY_i [P] with c_i = min(1, C / norms[i])."""
     B, T, d_in, d_out = _bt_dims(X, dY)
-    r = int(P.shape[1]) if P is not None else 0
+    r = _projection_width(P, X, d_out)
+    _holds_fp32(norms, "norms", B)
+    _holds_fp32(G_sum, "G_sum", d_in * (r or d_out))
     ws = _workspace(X, dY, r, workspace)
     check(lib().dp_clip_accumulate(_ptr(X), _ptr(dY), _ptr(P), r, _dtype_code(X), B, T, d_in, d_out,
                                    _ptr(norms), float(C), _ptr(G_sum), _ptr(ws), ws.numel(),
@@ -306,9 +326,11 @@ def dp_linear_step(X, dY, C, sigma, seed, step, layer_id, P=None, r=0, method="a
 
     B, T, d_in, d_out = _bt_dims(X, dY)
     if P is not None:
-        r = int(P.shape[1])
-    ws = _workspace(X, dY, r, workspace, method)
+        r = _projection_width(P, X, d_out)
     width = r if r else d_out
+    _holds_fp32(G_out, "G_out", d_in * width)
+    _holds_fp32(norms_out, "norms_out", B)
+    ws = _workspace(X, dY, r, workspace, method)
     if G_out is None:
         G_out = torch.empty(d_in, width, dtype=torch.float32, device=X.device)
     if norms_out is None:
@@ -398,11 +420,13 @@ def dp_block_step(layers, mode="per_layer", C=1.0, sigma=0.0, seed=0, step=0, me
     for k, l in enumerate(layers):
         _, _, d_in, d_out = _bt_dims(l["X"], l["dY"])
         P = l.get("P")
-        r = int(P.shape[1]) if P is not None else 0
+        r = _projection_width(P, l["X"], d_out)
         G = l.get("G_out")
         if G is None:
             G = torch.empty(d_in, r or d_out, dtype=torch.float32, device=l["X"].device)
         n = l.get("norms_out")
+        _holds_fp32(G, "G_out", d_in * (r or d_out))
+        _holds_fp32(n, "norms_out", B)
         arr[k] = DpLayer(_ptr(l["X"]), _ptr(l["dY"]), d_in, d_out, int(l["layer_id"]), float(l.get("C", C)),
                          _ptr(G), _ptr(n), _ptr(P), r)
         outs.append(G)
