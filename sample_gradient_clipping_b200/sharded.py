@@ -35,11 +35,12 @@ class LibraryOps:
         self.method = method
         self._ws = None   # one workspace, grown to the largest linear seen
 
-    def _workspace(self, X, dY):
+    def _workspace(self, X, dY, P=None):
         import torch
 
         B, T, d_in, d_out = (int(v) for v in (X.shape[0], X.shape[1], X.shape[2], dY.shape[2]))
-        need = self._lib.workspace_size(B, T, d_in, d_out, 0, self._lib._dtype_code(X), self.method)
+        r = int(P.shape[1]) if P is not None else 0
+        need = self._lib.workspace_size(B, T, d_in, d_out, r, self._lib._dtype_code(X), self.method)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=X.device)
         return self._ws
@@ -59,9 +60,10 @@ class LibraryOps:
                                                           stream=stream, **self._norm(layer))
             layer["G_out"], layer["norms_out"] = G, n
             return G
-        G, n = self._lib.dp_linear_step(layer["X"], layer["dY"], C, 0.0, seed, step, layer["layer_id"],
+        P = layer.get("P")
+        G, n = self._lib.dp_linear_step(layer["X"], layer["dY"], C, 0.0, seed, step, layer["layer_id"], P=P,
                                         method=self.method, norms_out=layer.get("norms_out"),
-                                        G_out=layer.get("G_out"), workspace=self._workspace(layer["X"], layer["dY"]),
+                                        G_out=layer.get("G_out"), workspace=self._workspace(layer["X"], layer["dY"], P),
                                         stream=stream)
         layer["G_out"], layer["norms_out"] = G, n
         return G
@@ -84,6 +86,15 @@ class LibraryOps:
     def _norm(layer):
         return {"eps": layer.get("eps", 1e-6), "residual_grad": layer.get("residual_grad")}
 
+    @staticmethod
+    def _sum_shape(layer):
+        if "ids" in layer:
+            return int(layer["V"]), int(layer["dY"].shape[2])
+        if "gain" in layer:
+            return tuple(layer["gain"].shape)
+        P = layer.get("P")
+        return int(layer["X"].shape[2]), int((layer["dY"] if P is None else P).shape[-1])
+
     def _mixed_sums(self, layers, C, stream):
         """Flat clipping over linears, tables and gains: every layer's norms first, then each
         layer's sum with the factors of the combined norms."""
@@ -91,6 +102,11 @@ class LibraryOps:
 
         import torch
 
+        for layer in layers:
+            G, shape = layer.get("G_out"), self._sum_shape(layer)
+            if G is not None and (tuple(G.shape) != shape or G.dtype != torch.float32):
+                raise ValueError(f"G_out of layer {layer['layer_id']} must be {torch.float32} of shape {list(shape)}, "
+                                 f"got {G.dtype} {list(G.shape)}")
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             for layer in layers:
                 if "ids" in layer:
@@ -101,25 +117,25 @@ class LibraryOps:
                         layer["H"], layer["gain"], layer["dY"], dX=layer.get("dX"), norms=layer.get("norms_out"),
                         **self._norm(layer))
                 else:
-                    n = self._lib.dp_per_sample_norms(layer["X"], layer["dY"], method=self.method,
+                    P = layer.get("P")
+                    n = self._lib.dp_per_sample_norms(layer["X"], layer["dY"], P=P, method=self.method,
                                                       norms=layer.get("norms_out"),
-                                                      workspace=self._workspace(layer["X"], layer["dY"]))
+                                                      workspace=self._workspace(layer["X"], layer["dY"], P))
                 layer["norms_out"] = n
             flat = torch.stack([layer["norms_out"] for layer in layers]).double().square().sum(0).sqrt().float()
             for layer in layers:
                 G = layer.get("G_out")
                 if G is None:
-                    shape = ((layer["V"], layer["dY"].shape[2]) if "ids" in layer else
-                             layer["gain"].shape if "gain" in layer else (layer["X"].shape[2], layer["dY"].shape[2]))
-                    G = torch.empty(shape, dtype=torch.float32, device=layer["dY"].device)
+                    G = torch.empty(self._sum_shape(layer), dtype=torch.float32, device=layer["dY"].device)
                 G.zero_()
                 if "ids" in layer:
                     self._lib.dp_embedding_clip_accumulate(layer["ids"], layer["dY"], flat, C, G, **self._embedding(layer))
                 elif "gain" in layer:
                     self._lib.dp_rmsnorm_clip_accumulate(layer["per_sample"], flat, C, G)
                 else:
-                    self._lib.dp_clip_accumulate(layer["X"], layer["dY"], flat, C, G,
-                                                 workspace=self._workspace(layer["X"], layer["dY"]))
+                    P = layer.get("P")
+                    self._lib.dp_clip_accumulate(layer["X"], layer["dY"], flat, C, G, P=P,
+                                                 workspace=self._workspace(layer["X"], layer["dY"], P))
                 layer["G_out"] = G
         return [layer["G_out"] for layer in layers], flat
 
@@ -131,7 +147,8 @@ def sharded_step(layers, sigma, seed, step, mode="per_layer", C=None, group=None
     """One privatised step of a block whose batch is split across the ranks of ``group``.
 
     ``layers``: this rank's shard, dicts with X [B_r, T, d_in], dY [B_r, T, d_out], layer_id, C
-    (per-layer bound) and optional G_out / norms_out.  Instead of X: ids [B_r, T] and V (and scale,
+    (per-layer bound) and optional G_out / norms_out / P (a projection [d_out, r], the same on every
+    rank: the linear's sum is then that of the projected gradients, [d_in, r]).  Instead of X: ids [B_r, T] and V (and scale,
     padding_idx) for an embedding table; H [B_r, T, d] and gain [d] (and eps, residual_grad) for an
     RMS norm, whose dX is then put into the dict.  ``mode``: "per_layer" (each linear its
     own C_l, noise sigma * C_l) or "flat" (bound ``C`` for the whole block, noise sigma * C).
