@@ -372,6 +372,8 @@ dp_status dp_embedding_step_dev_step(const void* ids, dp_index it, const void* d
  *   n_i = ||g_i||, c_i = min(1, C/n_i), sum_i c_i g_i + sigma*C*z with z over the d columns.
  *   - gain is DEVICE fp32 [d].  The other tensors are in dt.  A row is at most 32 KB (d <= 16384
  *     in bf16, 8192 in fp32; DP_ERR_UNSUPPORTED above), B <= 65535, eps >= 0 and finite.
+ *   - The sum of a row's squares is fp32, so it has to be below 3.4e38, and above 1.2e-38 where eps is
+ *     0 (rows of rms 1e-15 .. 1e16 are, at every width).
  *   - Outputs must not be inputs of the same call (DP_ERR_INVALID_ARG).
  *   - Results are the same bits on every run. */
 

@@ -1,7 +1,7 @@
 // RMS norm with the residual's addition, its backward, and the privatised gradient of its gain.
 //
 //   h = round(x + res),  r = 1 / sqrt(mean_j h_j^2 + eps),  y_j = h_j r g_j;
-//   backward, u_j = g_j dy_j:  dh_j = r u_j - h_j r^3 mean_k(u_k h_k)  (+ the gradient that
+//   backward, u_j = g_j dy_j:  dh_j = r (u_j - h_j r mean_k(u_k h_k r))  (+ the gradient that
 //   reaches h past the norm);
 //   sample i's gain gradient  g_i[j] = sum_t dy_tj h_tj r_t,  n_i = ||g_i||,
 //   S[j] = sum_i c_i g_i[j] + sigma C z_j.
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1)
     hh = __shfl_sync(0xFFFFFFFFu, both, 0);
     uh = __shfl_sync(0xFFFFFFFFu, both, 16);
     const float inv = 1.0f / sqrtf(fmaf(hh, inv_d, eps));
-    const float c = inv * inv * inv * (uh * inv_d);
+    const float mean = inv * (uh * inv_d);  // of u_j h_j r: like u in size, where r^3 may be out of range
     const long long out_at = base + static_cast<long long>(s) * d;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1)
       if constexpr (!kGainHeld) gains(k, w);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        acc[k][j] = fmaf(y[j], h[j] * inv, acc[k][j]);
-        const float dh = fmaf(inv, y[j] * (kGainHeld ? g[kGainHeld ? k : 0][j] : w[j]), -(h[j] * c));
+        const float x = h[j] * inv;
+        acc[k][j] = fmaf(y[j], x, acc[k][j]);
+        const float dh = inv * fmaf(-x, mean, y[j] * (kGainHeld ? g[kGainHeld ? k : 0][j] : w[j]));
         o[j] = RES ? o[j] + dh : dh;
       }
       if (DP_DCHECK(first + s < T_len, 51u, status)) reinterpret_cast<uint4*>(dX + out_at)[v] = pack16<T, V>(o, H);
