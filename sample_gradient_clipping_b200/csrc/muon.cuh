@@ -538,7 +538,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
   } else if constexpr (SPLIT) {
     // ------------------------------------------------------------ this CTA's part of the tile to the owners
     const int wq = warp & 3, half = (warp - 2) >> 2;
-    const bool ok = mbar_wait_bounded(smem_addr(acc_full), 0u, abort_flag, p.status, 24u);
+    const bool ok = mbar_wait_warp(smem_addr(acc_full), 0u, abort_flag, p.status, 24u);
     tc_fence_after();
     const int rows = 128 / shares, owner = 32 * wq / rows, row = 32 * wq % rows + static_cast<int>(lane);
     // parts[share][column][row]: a column of the warp's 32 rows is 128 contiguous bytes.
@@ -568,7 +568,7 @@ __device__ __forceinline__ void ns_body(const NsParams& p) {
       const int r0 = w.mb * Cfg::TILE + static_cast<int>(rank) * Cfg::BM + wq * 32;
       NsPlanes planes;
       if constexpr (Cfg::KIND == kNsApply) ns_load_planes(p, r0, w.nb * Cfg::TILE + half * (Cfg::TILE / 2), lane, planes);
-      if (!mbar_wait_bounded(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 24u)) break;
+      if (!mbar_wait_warp(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 24u)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + buf * 256 + (static_cast<uint32_t>(wq * 32) << 16);
       ns_epilogue<Cfg>(p, w, r0, tacc, half, turn, lane, delta, planes);
@@ -728,6 +728,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
     fence_mbar_init();
   }
   if (warp == 0) {
+    __syncwarp();
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
     tc_fence_before();
@@ -798,9 +799,11 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
       for (int j = 0; j < 32; ++j) v[j] = turn[lane][j];
       __syncwarp();
     }
+    __syncwarp();
     tmem_st32(tm_x + 64 * cc + 32 * half, v);
     put_hi(cc, v);
   }
+  __syncwarp();
   tmem_st_wait();
 
   uint32_t parity = 0;
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
       umma_commit(smem_addr(&done));
     }
     __syncwarp();
-    mbar_wait_bounded(smem_addr(&done), parity, &abort_word, p.status, 41u);
+    mbar_wait_warp(smem_addr(&done), parity, &abort_word, p.status, 41u);
     parity ^= 1u;
     tc_fence_after();
   };
@@ -836,6 +839,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         float v[32];
+        __syncwarp();
         tmem_ld32(tm_acc + 64 * half + 32 * part, v);
         tmem_ld_wait();
 #pragma unroll
@@ -849,6 +853,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         float v[32];
+        __syncwarp();
         tmem_ld32(tm_acc + 64 * half + 32 * part, v);
         tmem_ld_wait();
         const int c0 = 64 * half + 32 * part;
@@ -906,6 +911,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       float v[32];
+      __syncwarp();
       tmem_ld32(tm_acc + 64 * half + 32 * part, v);
       tmem_ld_wait();
 #pragma unroll
@@ -944,6 +950,7 @@ __global__ void __launch_bounds__(kNsSmallThreads, 1) ns_small_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = fmaf(kNsA + delta, x[j], v[j]);
       if (!last) {
+        __syncwarp();
         tmem_st32(tm_x + 64 * cc + 32 * half, v);
         put_hi(cc, v);
         continue;

@@ -126,6 +126,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same by a whole converged warp, which leaves it converged and of one mind: .sync.aligned
+// instructions and __syncwarp may follow, whichever lane's wait ran out.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                               uint32_t where) {
+  const bool ok = mbar_wait_bounded(bar, parity, abort, status, where);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
 // ---------------------------------------------------------------- TMA (tile mode, no cluster)
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");

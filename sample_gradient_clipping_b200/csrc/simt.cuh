@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(ReduceTmaConfig<BU>::THREADS, 1) clip_reduce_t
         asm volatile("bar.sync 1, %0;" ::"r"(32 * kReduceComputeWarps) : "memory");
         need_c = false;
       }
-      if (!mbar_wait_bounded(smem_addr(full + stage), phase, abort_flag, status, 22u)) break;
+      if (!mbar_wait_warp(smem_addr(full + stage), phase, abort_flag, status, 22u)) break;
       if (e < mn) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const uint8_t* base = smem + stage * Cfg::STAGE_BYTES + 16 * t;

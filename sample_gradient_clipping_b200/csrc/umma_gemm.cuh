@@ -713,7 +713,7 @@ __device__ __forceinline__ void umma_body(const UmmaParams& p, const UmmaGroup* 
     uint32_t buf_phase = 0;
     for (int u = blockIdx.x; u < p.num_units; u += gridDim.x) {
       const Unit w = decode_unit<Cfg>(p, u, grp);
-      if (!mbar_wait_bounded(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 4u)) break;
+      if (!mbar_wait_warp(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 4u)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + buf * Cfg::ACC_COLS + (static_cast<uint32_t>(wq * 32) << 16);
       epilogue_unit<Cfg>(p, w, tacc, wq, lane, grp);

@@ -299,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     uint32_t buf_phase = 0;
     for (int u = pair; u < p.num_units; u += num_pairs) {
       Unit w = decode_unit_pair<Cfg>(p, u);
-      if (!mbar_wait_bounded(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 14u)) break;
+      if (!mbar_wait_warp(smem_addr(acc_full + buf), buf_phase, abort_flag, p.status, 14u)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + buf * Cfg::ACC_COLS + (static_cast<uint32_t>(wq * 32) << 16);
       // Present this CTA's 128 rows to the one-SM epilogue: a 128-row tile with index
