@@ -445,6 +445,8 @@ dp_status dp_orthogonalize(const void* G, dp_dtype dt, int rows, int cols, int s
  *   g = grad_scale R (grad_scale = 1/B averages over the batch),  M <- momentum M + g,
  *   X = the orthogonalised (nesterov ? g + momentum M : M),
  *   W <- (1 - lr weight_decay) W - lr update_scale X.
+ * The first launch updates M, the last one W: after DP_ERR_CUDA M may have advanced without W, so a
+ * step that is to be made again needs the caller's own copy of M.
  *   W, M : DEVICE fp32, updated in place (M zeros before the first step); R : DEVICE fp32, the
  *   privatised gradient (G_out of an unprojected dp_linear_step); three different buffers.
  *   lr >= 0, 0 <= momentum < 1, weight_decay >= 0; a shape-dependent factor goes in

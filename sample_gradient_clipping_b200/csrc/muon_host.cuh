@@ -59,30 +59,43 @@ dp_status map_f16(CUtensorMap* map, const __half* base, int rows, int cols, uint
 }
 
 template <class Cfg>
-dp_status launch_ns(NsParams p, cudaStream_t stream, int shares = 1) {
-  auto kernel = [] {
-    if constexpr (Cfg::PAIR)
-      return ns_pair_kernel<Cfg>;
-    else
-      return ns_kernel<Cfg>;
-  }();
+constexpr auto ns_entry() {
+  if constexpr (Cfg::PAIR)
+    return ns_pair_kernel<Cfg>;
+  else
+    return ns_kernel<Cfg>;
+}
+
+template <class Cfg>
+dp_status ns_configure() {
   static std::atomic<bool> configured[64] = {};
   int dev = 0;
   DP_CUDA(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    DP_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES));
+    DP_CUDA(cudaFuncSetAttribute(ns_entry<Cfg>(), cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES));
     if (dev >= 0 && dev < 64) configured[dev].store(true);
   }
+  return DP_OK;
+}
+
+template <class Cfg>
+dp_status ns_launch(NsParams p, cudaStream_t stream, int shares) {
   const int ctas = Cfg::PAIR ? 2 : 1;
   const int grid = Cfg::SPLIT ? p.num_units * shares : std::min(p.num_units, sm_count() / ctas) * ctas;
   p.early = 2 * grid <= sm_count() ? 1 : 0;
   LaunchScope scope(kKindNsProduct, stream);
-  DP_LAUNCH_CLUSTER("ns_kernel", Cfg::SPLIT ? shares : 0, kernel, grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
+  DP_LAUNCH_CLUSTER("ns_kernel", Cfg::SPLIT ? shares : 0, ns_entry<Cfg>(), grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
   return DP_OK;
 }
 
+// The form of a product: 256 x 256 tiles on SM pairs or 128 x 128 on SMs, and the SMs that share a tile.
+struct NsForm {
+  bool pair;
+  int shares, tiles_m, tiles_n, units;
+};
+
 template <int KIND>
-dp_status ns_product(NsParams p, cudaStream_t stream) {
+NsForm ns_form(const NsParams& p) {
   auto units = [&](int tile, int* tm, int* tn) {
     *tm = ceil_div(p.m, tile);
     *tn = ceil_div(p.n, tile);
@@ -91,25 +104,34 @@ dp_status ns_product(NsParams p, cudaStream_t stream) {
   };
   int tm2, tn2, tm1, tn1;
   const int u2 = units(256, &tm2, &tn2), u1 = units(128, &tm1, &tn1);
-  // A wave of 256 x 256 tiles on SM pairs and a wave of 128 x 128 tiles on SMs take about as long
-  // (each CTA streams 32 KB a K block); the small tiles' epilogue is half as long.
-  const bool pair = ceil_div(u2, sm_count() / 2) < ceil_div(u1, sm_count());
-  p.tiles_m = pair ? tm2 : tm1;
-  p.tiles_n = pair ? tn2 : tn1;
-  p.num_units = pair ? u2 : u1;
   if constexpr (KIND != kNsApply) {
     // Few tiles: their K blocks (0.28 us each) are shared by 4 or 2 SMs a tile, where that saves more
     // than the exchange of the parts costs (about 2 us).  Clusters of 4 leave some SMs of a group unused:
     // 36 of them did not fit at once (1024 x 1024: 193 us against 140 unsplit), 32 do.
     const int shares = u1 * 4 <= 128 && p.k_blocks >= 16 ? 4 : u1 * 2 <= sm_count() && p.k_blocks >= 24 ? 2 : 1;
-    if (shares > 1) {
-      p.tiles_m = tm1;
-      p.tiles_n = tn1;
-      p.num_units = u1;
-      return launch_ns<NsConfig<false, KIND, true>>(p, stream, shares);
-    }
+    if (shares > 1) return NsForm{false, shares, tm1, tn1, u1};
   }
-  return pair ? launch_ns<NsConfig<true, KIND>>(p, stream) : launch_ns<NsConfig<false, KIND>>(p, stream);
+  // A wave of 256 x 256 tiles on SM pairs and a wave of 128 x 128 tiles on SMs take about as long
+  // (each CTA streams 32 KB a K block); the small tiles' epilogue is half as long.
+  const bool pair = ceil_div(u2, sm_count() / 2) < ceil_div(u1, sm_count());
+  return pair ? NsForm{true, 1, tm2, tn2, u2} : NsForm{false, 1, tm1, tn1, u1};
+}
+
+// A product in its form: configured (before the call's first launch), or launched.
+template <int KIND>
+dp_status ns_product(NsParams p, cudaStream_t stream, bool configure) {
+  const NsForm f = ns_form<KIND>(p);
+  p.tiles_m = f.tiles_m;
+  p.tiles_n = f.tiles_n;
+  p.num_units = f.units;
+  auto run = [&](auto cfg) {
+    using Cfg = decltype(cfg);
+    return configure ? ns_configure<Cfg>() : ns_launch<Cfg>(p, stream, f.shares);
+  };
+  if constexpr (KIND != kNsApply) {
+    if (f.shares > 1) return run(NsConfig<false, KIND, true>{});
+  }
+  return f.pair ? run(NsConfig<true, KIND>{}) : run(NsConfig<false, KIND>{});
 }
 
 struct MuonOut {
@@ -204,56 +226,32 @@ dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs,
   const long long vecs = total / EmbVec<T>::N;
   const int most = std::min(sm_count() * kMuonBlocksPerSm, kMuonMaxBlocks);
   const int blocks = static_cast<int>(std::min<long long>(most, (vecs + 4 * kMuonThreads - 1) / (4 * kMuonThreads)));
-  {
-    LaunchScope scope(kKindMuonMomentum, stream);
-    DP_LAUNCH("muon_momentum_kernel", (muon_momentum_kernel<T, MUON>), blocks, kMuonThreads, 0, stream, R, M, vecs, mu, gs,
-              nesterov ? 1 : 0, partials, status);
-  }
+
+  // What can fail on the host comes first: the first launch changes the caller's momentum.
   bool wide = false;
   if (m <= kNsSmallRows && (st = ns_small_configure<T, MUON>(&wide)) != DP_OK) return st;
-  if (const int ctas = ns_small_ctas(m, n, wide))
-    return ns_small<T, MUON>(R, M, rows, cols, mu, gs, nesterov, steps, out, partials, blocks, ctas, status, stream);
-  {
-    LaunchScope scope(kKindMuonPrepare, stream);
-    if (tall) {
-      const long long tiles = static_cast<long long>(ceil_div(rows, 64)) * ceil_div(cols, 64);
-      DP_LAUNCH("muon_prepare_kernel", (muon_prepare_kernel<T, MUON, true>), static_cast<int>(std::min<long long>(tiles, most)),
-                kMuonThreads, 0, stream, R, M, rows, cols, mu, gs, nesterov ? 1 : 0, partials, blocks, plane(L.hi[0]),
-                plane(L.lo[0]));
-    } else {
-      const long long want = (total / 2 + 4 * kMuonThreads - 1) / (4 * kMuonThreads);
-      DP_LAUNCH("muon_prepare_kernel", (muon_prepare_kernel<T, MUON, false>), static_cast<int>(std::min<long long>(want, most)),
-                kMuonThreads, 0, stream, R, M, rows, cols, mu, gs, nesterov ? 1 : 0, partials, blocks, plane(L.hi[0]),
-                plane(L.lo[0]));
-    }
-  }
-  CUtensorMap xk[2], xn[2], ak, bk;
-  for (int k = 0; k < 2; ++k) {
-    if ((st = map_f16(&xk[k], plane(L.hi[k]), m, n, 128)) != DP_OK) return st;
-    if ((st = map_f16(&xn[k], plane(L.hi[k]), m, n, 64)) != DP_OK) return st;
-  }
-  if ((st = map_f16(&ak, plane(L.A), m, m, 128)) != DP_OK) return st;
-  if ((st = map_f16(&bk, plane(L.B), m, m, 128)) != DP_OK) return st;
+  const int ctas = ns_small_ctas(m, n, wide);
+  CUtensorMap xk[2] = {}, xn[2] = {}, ak = {}, bk = {};
   NsParams base;
   memset(&base, 0, sizeof(base));
   base.trace = reinterpret_cast<float*>(ws + L.trace);
   base.order = m;
   base.status = status;
-  for (int s = 0; s < steps; ++s) {
+  auto products = [&](int s, bool configure) {
     const int x = s & 1;
     NsParams g = base;
     g.tmA = g.tmB = xk[x];
     g.m = g.n = m;
     g.k_blocks = ceil_div(n, 64);
     g.out = plane(L.A);
-    if ((st = ns_product<kNsGram>(g, stream)) != DP_OK) return st;
+    if ((st = ns_product<kNsGram>(g, stream, configure)) != DP_OK) return st;
     NsParams q = base;
     q.tmA = q.tmB = ak;
     q.m = q.n = m;
     q.k_blocks = ceil_div(m, 64);
     q.A = plane(L.A);
     q.out = plane(L.B);
-    if ((st = ns_product<kNsPoly>(q, stream)) != DP_OK) return st;
+    if ((st = ns_product<kNsPoly>(q, stream, configure)) != DP_OK) return st;
     NsParams a = base;
     a.tmA = bk;
     a.tmB = xn[x];
@@ -271,8 +269,41 @@ dp_status muon_run(const T* R, float* M, int rows, int cols, float mu, float gs,
       a.keep = out.keep;
       a.rate = out.rate;
     }
-    if ((st = ns_product<kNsApply>(a, stream)) != DP_OK) return st;
+    return ns_product<kNsApply>(a, stream, configure);
+  };
+  if (!ctas) {
+    for (int k = 0; k < 2; ++k) {
+      if ((st = map_f16(&xk[k], plane(L.hi[k]), m, n, 128)) != DP_OK) return st;
+      if ((st = map_f16(&xn[k], plane(L.hi[k]), m, n, 64)) != DP_OK) return st;
+    }
+    if ((st = map_f16(&ak, plane(L.A), m, m, 128)) != DP_OK) return st;
+    if ((st = map_f16(&bk, plane(L.B), m, m, 128)) != DP_OK) return st;
+    if ((st = products(0, true)) != DP_OK) return st;  // every step's products have the same forms
   }
+
+  {
+    LaunchScope scope(kKindMuonMomentum, stream);
+    DP_LAUNCH("muon_momentum_kernel", (muon_momentum_kernel<T, MUON>), blocks, kMuonThreads, 0, stream, R, M, vecs, mu, gs,
+              nesterov ? 1 : 0, partials, status);
+  }
+  if (ctas)
+    return ns_small<T, MUON>(R, M, rows, cols, mu, gs, nesterov, steps, out, partials, blocks, ctas, status, stream);
+  {
+    LaunchScope scope(kKindMuonPrepare, stream);
+    if (tall) {
+      const long long tiles = static_cast<long long>(ceil_div(rows, 64)) * ceil_div(cols, 64);
+      DP_LAUNCH("muon_prepare_kernel", (muon_prepare_kernel<T, MUON, true>), static_cast<int>(std::min<long long>(tiles, most)),
+                kMuonThreads, 0, stream, R, M, rows, cols, mu, gs, nesterov ? 1 : 0, partials, blocks, plane(L.hi[0]),
+                plane(L.lo[0]));
+    } else {
+      const long long want = (total / 2 + 4 * kMuonThreads - 1) / (4 * kMuonThreads);
+      DP_LAUNCH("muon_prepare_kernel", (muon_prepare_kernel<T, MUON, false>), static_cast<int>(std::min<long long>(want, most)),
+                kMuonThreads, 0, stream, R, M, rows, cols, mu, gs, nesterov ? 1 : 0, partials, blocks, plane(L.hi[0]),
+                plane(L.lo[0]));
+    }
+  }
+  for (int s = 0; s < steps; ++s)
+    if ((st = products(s, false)) != DP_OK) return st;
   return DP_OK;
 }
 
