@@ -641,6 +641,8 @@ def dp_embedding_step(ids, dY, V, C, sigma, seed, step, layer_id, scale=1.0, pad
     """The privatised gradient of an embedding table of V rows; returns (G_out [V, d], norms_out).
 
     ``ids`` [B, T] int32 or int64, ``dY`` [B, T, d]; ``step`` as in dp_linear_step.
+    An id >= V is recorded in the workspace's status word, so a caller who wants to know brings the
+    workspace (embedding_workspace_size) and asks dp_workspace_status.
     """
     import torch
 

@@ -50,14 +50,14 @@ class LibraryOps:
         if "ids" in layer:
             G, n = self._lib.dp_embedding_step(layer["ids"], layer["dY"], layer["V"], C, 0.0, seed, step,
                                                layer["layer_id"], norms_out=layer.get("norms_out"),
-                                               G_out=layer.get("G_out"), stream=stream, **self._embedding(layer))
+                                               G_out=layer.get("G_out"), stream=stream, **self._embedding(layer, stream))
             layer["G_out"], layer["norms_out"] = G, n
             return G
         if "gain" in layer:
             layer["dX"], G, n = self._lib.dp_rmsnorm_step(layer["H"], layer["gain"], layer["dY"], C, 0.0, seed, step,
                                                           layer["layer_id"], dX=layer.get("dX"),
                                                           norms_out=layer.get("norms_out"), G_out=layer.get("G_out"),
-                                                          stream=stream, **self._norm(layer))
+                                                          stream=stream, **self._norm(layer, stream))
             layer["G_out"], layer["norms_out"] = G, n
             return G
         P = layer.get("P")
@@ -79,12 +79,30 @@ class LibraryOps:
         return outs, flat
 
     @staticmethod
-    def _embedding(layer):
-        return {"scale": layer.get("scale", 1.0), "padding_idx": layer.get("padding_idx")}
+    def _kept_workspace(layer, need, stream):
+        """The layer's workspace, made where it has none of `need` bytes and kept in its dict, as its
+        sums are: its status word can then be read after the step (layer_status)."""
+        import contextlib
 
-    @staticmethod
-    def _norm(layer):
-        return {"eps": layer.get("eps", 1e-6), "residual_grad": layer.get("residual_grad")}
+        import torch
+
+        ws, device = layer.get("workspace"), layer["dY"].device
+        if need and (ws is None or ws.numel() * ws.element_size() < need or ws.device != device):
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                ws = layer["workspace"] = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws
+
+    def _embedding(self, layer, stream=None):
+        B, T, d = (int(v) for v in layer["dY"].shape)
+        need = self._lib.embedding_workspace_size(B, T, int(layer["V"]), d, self._lib._dtype_code(layer["dY"]))
+        return {"scale": layer.get("scale", 1.0), "padding_idx": layer.get("padding_idx"),
+                "workspace": self._kept_workspace(layer, need, stream)}
+
+    def _norm(self, layer, stream=None):
+        B, T, d = (int(v) for v in layer["dY"].shape)
+        need = self._lib.rmsnorm_workspace_size(B, T, d, self._lib._dtype_code(layer["dY"]))
+        return {"eps": layer.get("eps", 1e-6), "residual_grad": layer.get("residual_grad"),
+                "workspace": self._kept_workspace(layer, need, stream)}
 
     @staticmethod
     def _sum_shape(layer):
@@ -150,7 +168,8 @@ def sharded_step(layers, sigma, seed, step, mode="per_layer", C=None, group=None
     (per-layer bound) and optional G_out / norms_out / P (a projection [d_out, r], the same on every
     rank: the linear's sum is then that of the projected gradients, [d_in, r]).  Instead of X: ids [B_r, T] and V (and scale,
     padding_idx) for an embedding table; H [B_r, T, d] and gain [d] (and eps, residual_grad) for an
-    RMS norm, whose dX is then put into the dict.  ``mode``: "per_layer" (each linear its
+    RMS norm, whose dX is then put into the dict.  The workspace of a table or a norm is kept in its
+    dict too (or given there): layer_status reads it.  ``mode``: "per_layer" (each linear its
     own C_l, noise sigma * C_l) or "flat" (bound ``C`` for the whole block, noise sigma * C).
     Every rank returns the same noisy global sums, one per linear, and its own samples' norms.
     """
@@ -185,6 +204,17 @@ def sharded_step(layers, sigma, seed, step, mode="per_layer", C=None, group=None
                 ops.add_noise(G, std, seed, step, layer["layer_id"])
             results.append(G)
     return results, [layer.get("norms_out") for layer in layers]
+
+
+def layer_status(layers, stream=None):
+    """What the kernels of a step recorded, layer by layer: the dp_status of each layer's workspace, None
+    for a layer that keeps none (linears).  DP_ERR_INVALID_ARG: a token id past the table's end, whose
+    tokens are missing from this rank's sum; DP_ERR_TIMEOUT: an in-kernel wait ran out, and the sum is
+    invalid.  Synchronises the stream (``stream``, or the current one)."""
+    from . import _lib
+
+    return [_lib.dp_workspace_status(layer["workspace"], stream) if layer.get("workspace") is not None else None
+            for layer in layers]
 
 
 def shard_rows(batch, rank, world):

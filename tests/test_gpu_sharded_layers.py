@@ -88,3 +88,21 @@ def test_projected_linear_beside_others_and_alone():
                                     C=1e6)
     for a, b in zip(mixed[2:], outs):
         assert a.shape == b.shape and rel_fro(host(a), host(b)) <= 2 * TOL["bf16"]["sum"]
+
+
+@pytest.mark.parametrize("mode", ["per_layer", "flat"])
+def test_an_id_past_the_table_is_reported_after_the_step(mode):
+    layers = _cuda(_layers(2))
+    for layer in layers:
+        layer["C"] = 1.0
+    sharded.sharded_step(layers, 0.0, 5, 6, mode=mode, C=1.0)
+    assert sharded.layer_status(layers) == [_lib.DP_OK, _lib.DP_OK, None, None]
+    spaces = [layer.get("workspace") for layer in layers]
+    good = layers[0]["ids"][2, 7].item()
+    layers[0]["ids"][2, 7] = V
+    sharded.sharded_step(layers, 0.0, 5, 6, mode=mode, C=1.0)
+    assert sharded.layer_status(layers) == [_lib.DP_ERR_INVALID_ARG, _lib.DP_OK, None, None]
+    assert all(a is b for a, b in zip(spaces, [layer.get("workspace") for layer in layers]))
+    layers[0]["ids"][2, 7] = good
+    sharded.sharded_step(layers, 0.0, 5, 6, mode=mode, C=1.0)
+    assert sharded.layer_status(layers) == [_lib.DP_OK, _lib.DP_OK, None, None]

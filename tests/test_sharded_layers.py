@@ -29,6 +29,14 @@ class OracleLibrary:
         return 256
 
     @staticmethod
+    def embedding_workspace_size(B, T, V, d, dtype_code):
+        return 1000 * B
+
+    @staticmethod
+    def rmsnorm_workspace_size(B, T, d, dtype_code):
+        return 500 * B
+
+    @staticmethod
     def _fill(out, value):
         value = torch.from_numpy(np.asarray(value))
         if out is None:
@@ -196,6 +204,45 @@ def test_a_projected_linear_is_the_same_beside_other_kinds(alone, mode):
     for a, b in zip(mixed[2:], linears):
         np.testing.assert_allclose(a, b, rtol=1e-12)
     assert [tuple(g.shape) for g in block] == [(DI, R), (DI, DO)]
+
+
+@pytest.mark.parametrize("mode", ["per_layer", "flat"])
+def test_workspaces_are_kept_and_their_status_read(alone, mode, monkeypatch):
+    """A table's and a norm's status words outlive the step: the same workspace in every call of it, made
+    again only where a larger batch needs more; a given one is used."""
+    used = []
+
+    class Library(OracleLibrary):
+        pass
+
+    for name in ("dp_embedding_step", "dp_embedding_per_sample_norms", "dp_embedding_clip_accumulate", "dp_rmsnorm_step",
+                 "dp_rmsnorm_backward"):
+        def call(self, *a, workspace=None, _real=getattr(OracleLibrary, name), **k):
+            used.append(workspace)
+            return _real(self, *a, **k)
+
+        setattr(Library, name, call)
+    ops = _ops()
+    ops._lib = Library()
+    layers = _batch()
+    for small in (True, False, False):
+        used.clear()
+        part = _share([{k: v for k, v in l.items() if k not in ("G_out", "norms_out", "dX", "per_sample", "workspace")}
+                       for l in layers], 0, 2 if small else B)
+        for mine, layer in zip(part, layers):
+            if "workspace" in layer:
+                mine["workspace"] = layer["workspace"]
+        sharded.sharded_step(part, 0.0, 0, 0, mode=mode, C=2.5, ops=ops)
+        assert [("workspace" in l) for l in part] == [True, True, False, False]
+        assert all(w is part[0]["workspace"] or w is part[1]["workspace"] for w in used if w is not None)
+        assert part[0]["workspace"].numel() == 1000 * (2 if small else B) and part[1]["workspace"].numel() == 500 * (2 if small else B)
+        if not small and layers[0].get("workspace") is not None and layers[0]["workspace"].numel() == 1000 * B:
+            assert part[0]["workspace"] is layers[0]["workspace"] and part[1]["workspace"] is layers[1]["workspace"]
+        for mine, layer in zip(part, layers):
+            if "workspace" in mine:
+                layer["workspace"] = mine["workspace"]
+    monkeypatch.setattr(_lib, "dp_workspace_status", lambda ws, stream=None: ws.numel())
+    assert sharded.layer_status(layers) == [1000 * B, 500 * B, None, None]
 
 
 class _Untouched:
