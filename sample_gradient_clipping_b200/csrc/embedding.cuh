@@ -502,6 +502,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kEmbSortThreads, 
 // kernel is a stream of dY rows and a warp needs bytes in flight: one sorted position a warp, one vector
 // a lane and a barrier between positions took 162 us for 8 x 2048 tokens of 4096 in bf16; this stream takes
 // 37 (134 MB at 3.6 TB/s), with two rows in flight 39, with four vectors a lane (half the blocks fit) 42.
+// Four blocks an SM leave 64 registers, and the bf16 form spills a little (68 bytes stored, 72 loaded a thread).
 constexpr int kEmbVecs = 2;
 // Sorted positions whose groups a warp takes.  Fewer spread short calls over more warps (4 x 16 tokens of 64:
 // 9.5 us with 16, 7.2 with 4; 16496 of 1032: 18.6 and 16.9; 16384 of 4096: 40 both; with 8: 7.5, 16.3 and 42).

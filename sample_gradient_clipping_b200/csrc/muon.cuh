@@ -9,7 +9,8 @@
 //
 // The products run on the tensor cores in fp16 with fp32 accumulation: all values are at most
 // about 1 here, so fp16's 11 bits serve where bf16 would keep 8.  Three choices keep five steps on a
-// noisy gradient within 1e-3 of the exact iteration (3e-3 without them, 1.5e-2 with bf16 operands):
+// noisy gradient within 1e-3 of the exact iteration (3e-3 without them, 1.5e-2 with bf16 operands; a bf16
+// result's own rounding is 1.7e-3):
 //   - X is held as two fp16 planes, hi + lo 2^-11.  Products read hi; the term a X, by which small
 //     singular values grow 3.4 times a step, uses both, so their rounding does not grow with them.
 //   - b A and c A^2 use the same rounded A, so the polynomial is exact in the matrix that is stored.
